@@ -22,12 +22,24 @@ Two levels:
     ``sync_backward_stats`` / ``sync_backward_apply`` (the C calls), and
     ``forward_sync`` / ``backward_sync``, which put ``gather_records`` (an
     all-gather over a torch.distributed group) between them.
+  * The row operators for transformer blocks (include/iabn_block.h):
+    ``block_norm_forward``, ``block_norm_backward``, ``gated_forward``,
+    ``gated_backward``, their ``_checkpoint8`` forms, ``checkpoint8_store`` and
+    ``checkpoint8_load``; see ``block``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+
+from .block import (  # noqa: F401
+    BLOCK_EXPORTS, IABN_BLOCK_MAX_COLS, IABN_GLU_GELU, IABN_GLU_GELU_TANH, IABN_GLU_SILU,
+    IABN_NORM_LAYER, IABN_NORM_NONE, IABN_NORM_RMS, IABN_Q8_E4M3, IABN_Q8_GROUP, IABN_Q8_INT8,
+    IabnBlockDesc, IabnGatedDesc, block_norm_backward, block_norm_backward_checkpoint8,
+    block_norm_forward, block_norm_forward_checkpoint8, block_norm_workspace_size,
+    checkpoint8_load, checkpoint8_store, declare, gated_backward, gated_backward_checkpoint8,
+    gated_forward, gated_forward_checkpoint8, new_block_norm_workspace)
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libiabn.so")
@@ -163,6 +175,7 @@ def lib() -> ctypes.CDLL:
             L.iabn_probe_read_write.restype = i32
             L.iabn_probe_cluster_occupancy.argtypes = [i32, i32, i32, ctypes.POINTER(i32)]
             L.iabn_probe_cluster_occupancy.restype = i32
+            declare(L)
             _lib = L
     return _lib
 
