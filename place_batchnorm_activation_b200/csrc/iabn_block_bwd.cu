@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
             Codes<VEC> c;
             float sc[2] = {0.f, 0.f};
             c.load(static_cast<const uint8_t*>(src) + row * D + c0, rw.lane, left);
-            if (left > 0) load_scales<VEC>(scales + row * p.groups, c0, rw.lane, left, sc);
+            load_scales<VEC>(scales + row * p.groups + c0 / kQGroup, rw.lane, left, sc);
             c.get(p.format, sc, f);
         } else {
             Raw<DT, VEC> r;

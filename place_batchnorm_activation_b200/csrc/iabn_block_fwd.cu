@@ -97,9 +97,12 @@ __global__ void __launch_bounds__(MAXT) block_fwd(const BlockFwd p, int row_warp
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-                if (p.q_post && left > 0)
-                    quantise8<VEC>(p.format, x[k], p.q_post + at + c0,
-                                   p.scale_post + row * p.groups, c0, rw.lane, left);
+                if (p.q_post && left > 0) {
+                    uint32_t m[2];
+                    group_amax<VEC>(x[k], m);
+                    quantise8<VEC>(p.format, x[k], m, p.q_post + at + c0,
+                                   p.scale_post + row * p.groups + c0 / kQGroup, rw.lane, left);
+                }
                 float g[kEl], ga[kEl], be[kEl];
                 load_param<VEC>(gate, c0, rw.lane, left, 1.f, g);
                 load_param<VEC>(p.gamma_post, c0, rw.lane, left, 1.f, ga);
@@ -120,9 +123,12 @@ __global__ void __launch_bounds__(MAXT) block_fwd(const BlockFwd p, int row_warp
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-                if (p.q_pre && left > 0)
-                    quantise8<VEC>(p.format, h[k], p.q_pre + at + c0, p.scale_pre + row * p.groups,
-                                   c0, rw.lane, left);
+                if (p.q_pre && left > 0) {
+                    uint32_t m[2];
+                    group_amax<VEC>(h[k], m);
+                    quantise8<VEC>(p.format, h[k], m, p.q_pre + at + c0,
+                                   p.scale_pre + row * p.groups + c0 / kQGroup, rw.lane, left);
+                }
                 float ga[kEl], be[kEl], o[kEl];
                 load_param<VEC>(p.gamma_pre, c0, rw.lane, left, 1.f, ga);
                 load_param<VEC>(p.beta_pre, c0, rw.lane, left, 0.f, be);

@@ -5,8 +5,7 @@
 // 2 sqrt(2/pi) (a + 0.044715 a^3) (GELU_TANH: (1 + tanh y)/2 = 1/(1 + e^-2y),
 // which does not cancel for large negative y), or the normal distribution
 // function (GELU), so phi' = w + a w'.
-// Elementwise; a warp takes 256 columns of a row at a time (two checkpoint
-// groups).  Bound: HBM bandwidth: 3 s bytes an element forward (2 more with
+// Elementwise; a warp takes 256 columns (two checkpoint groups) of many rows.  Bound: HBM bandwidth: 3 s bytes an element forward (2 more with
 // checkpoints), 3 s + 2 backward from codes, s more for z.
 #include "iabn_rows.cuh"
 
@@ -16,13 +15,25 @@ void count_launches(int n);
 
 namespace {
 
+// e^x and 1/x for the 16-bit types: one special-function instruction each
+// (relative error about 2^-22 and 2^-23), results below 2^-126 flushed to 0.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <int DT>
 __device__ __forceinline__ float exp_of(float x) {
-    return DT == kF32 ? expf(x) : __expf(x);
+    return DT == kF32 ? expf(x) : fast_exp2(x * 1.4426950408889634f);
 }
 template <int DT>
 __device__ __forceinline__ float inverse(float x) {   // of 1 + e^y: in [1, inf]
-    return DT == kF32 ? 1.f / x : __fdividef(1.f, x);
+    return DT == kF32 ? 1.f / x : fast_inverse(x);
 }
 
 // w(a), and a w'(a) where SLOPE.
@@ -44,203 +55,336 @@ __device__ __forceinline__ void weight(float a, float& w, float& aw) {
     }
 }
 
-// Rows and segments of a warp's walk over [rows, cols] in steps of all warps.
-struct Walk {
-    int64_t row;
-    int seg;
-    int64_t drow;
-    int dseg, segs;
-    __device__ __forceinline__ Walk(int64_t cols) {
-        segs = (int)((cols + kSeg - 1) / kSeg);
-        const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-        const int64_t at = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-        row = at / segs;
-        seg = (int)(at - row * segs);
-        drow = warps / segs;
-        dseg = (int)(warps - drow * segs);
-    }
-    __device__ __forceinline__ void next() {
-        row += drow;
-        seg += dseg;
-        if (seg >= segs) {
-            seg -= segs;
-            ++row;
-        }
-    }
+// A warp's share of [rows, cols]: one segment of columns (so that what goes by
+// column is read once) of every `lanes`-th row, from `row` on; consecutive
+// warps hold consecutive segments of a row.  Where there are more segments
+// than warps, a warp takes several in turn.
+struct Strip {
+    int segs, lanes;
 };
 
-template <int DT, bool VEC, int ACT>
-__global__ void __launch_bounds__(256) gated_fwd(const Gated p) {
+template <class F>
+__device__ __forceinline__ void for_strips(const Strip& t, int64_t cols, F body) {
+    const int64_t all = (int64_t)t.segs * t.lanes;
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+    for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < all; w += warps) {
+        const int64_t row = w / t.segs;
+        const int64_t c0 = (w - row * t.segs) * kSeg;
+        body(row, c0, (int)min(cols - c0, (int64_t)kSeg));
+    }
+}
+
+// An offset that walks down a strip of a tensor with row stride ld: [i] is i
+// rows of the strip ahead.  Tensors of one stride share it.
+struct Down {
+    int64_t at, step;
+    __device__ __forceinline__ Down(int64_t row, int64_t ld, int64_t col, int lanes)
+        : at(row * ld + col), step(ld * lanes) {}
+    __device__ __forceinline__ int64_t operator[](int i) const { return at + i * step; }
+    __device__ __forceinline__ void advance(int n) { at += n * step; }
+};
+
+// Rows of a strip that are loaded before any is worked on, and blocks an SM:
+// with fewer bytes in flight HBM waits, with more the registers run out (8192 x
+// 14336 bf16, int8 checkpoints, forward: 2 rows and 4 blocks 182 us; 1 and 4
+// 193, 1 and 6 195, 2 and 3 189, 4 and 2 194, 4 and 3 186).  Elements one by
+// one take eight times the load instructions, so one row is ahead enough
+// (777 x 2731: 10.4 us, 13.1 with two).
+constexpr int kVecAhead = 2;
+constexpr int kNoCodes = -1;   // in place of a checkpoint format
+constexpr int kBlocks = 4;
+
+template <int DT, bool VEC, int ACT, int FMT>
+__global__ void __launch_bounds__(256, kBlocks) gated_fwd(const Gated p, const Strip t) {
+    constexpr int kAhead = VEC ? kVecAhead : 1;
     using T = typename Storage<DT>::T;
     const int lane = threadIdx.x & 31;
     const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
-    for (Walk k(p.cols); k.row < p.rows; k.next()) {
-        const int64_t c0 = (int64_t)k.seg * kSeg;
-        const int left = (int)min(p.cols - c0, (int64_t)kSeg);
-        Raw<DT, VEC> ra, rb;
-        ra.load(static_cast<const T*>(p.a) + k.row * p.ld + c0, lane, left);
-        rb.load(static_cast<const T*>(p.b) + k.row * p.ld + c0, lane, left);
-        float a[kEl], b[kEl], z[kEl];
-        ra.get(a);
-        rb.get(b);
+    for_strips(t, p.cols, [&](int64_t row0, int64_t c0, int left) {
+        Down in(row0, p.ld, c0, t.lanes), out(row0, p.cols, c0, t.lanes);
+        Down grp(row0, groups, c0 / kQGroup, t.lanes);
+        const T *pa = static_cast<const T*>(p.a), *pb = static_cast<const T*>(p.b);
+        T* pz = static_cast<T*>(p.z);
+        for (int64_t rows = p.rows - row0; rows > 0; rows -= kAhead * t.lanes) {
+            Raw<DT, VEC> ra[kAhead], rb[kAhead];
+            bool on[kAhead];
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) {
-            float w, aw;
-            weight<ACT, DT, false>(a[j], w, aw);
-            z[j] = a[j] * w * b[j];
-        }
-        store8<DT, VEC>(static_cast<T*>(p.z) + k.row * p.cols + c0, lane, left, z);
-        if (p.qa_out) {
-            const int64_t at = k.row * p.cols + c0;
-            quantise8<VEC>(p.format, a, p.qa_out + at, p.sa_out + k.row * groups, c0, lane, left);
-            quantise8<VEC>(p.format, b, p.qb_out + at, p.sb_out + k.row * groups, c0, lane, left);
-        }
-    }
-}
-
-template <int DT, bool VEC, int ACT, bool CODES>
-__global__ void __launch_bounds__(256) gated_bwd(const Gated p) {
-    using T = typename Storage<DT>::T;
-    const int lane = threadIdx.x & 31;
-    const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
-    for (Walk k(p.cols); k.row < p.rows; k.next()) {
-        const int64_t c0 = (int64_t)k.seg * kSeg;
-        const int left = (int)min(p.cols - c0, (int64_t)kSeg);
-        const int64_t at = k.row * p.cols + c0;
-        float a[kEl], b[kEl], dz[kEl];
-        Raw<DT, VEC> rz;
-        rz.load(static_cast<const T*>(p.dz) + at, lane, left);
-        if (CODES) {
-            Codes<VEC> qa, qb;
-            float sa[2], sb[2];
-            qa.load(p.qa + at, lane, left);
-            qb.load(p.qb + at, lane, left);
-            load_scales<VEC>(p.sa + k.row * groups, c0, lane, left, sa);
-            load_scales<VEC>(p.sb + k.row * groups, c0, lane, left, sb);
-            qa.get(p.format, sa, a);
-            qb.get(p.format, sb, b);
-        } else {
-            Raw<DT, VEC> ra, rb;
-            ra.load(static_cast<const T*>(p.a) + k.row * p.ld + c0, lane, left);
-            rb.load(static_cast<const T*>(p.b) + k.row * p.ld + c0, lane, left);
-            ra.get(a);
-            rb.get(b);
-        }
-        rz.get(dz);
-        float da[kEl], db[kEl], z[kEl];
+            for (int i = 0; i < kAhead; ++i) {
+                on[i] = rows > i * t.lanes;
+                ra[i].load(pa + in[i], lane, on[i] ? left : 0);
+                rb[i].load(pb + in[i], lane, on[i] ? left : 0);
+            }
+            float by[2 * kAhead];
+            if constexpr (FMT != kNoCodes && VEC) {
+                const uint32_t m[4] = {raw_amax(ra[0]), raw_amax(rb[0]), raw_amax(ra[1]), raw_amax(rb[1])};
+                float* const s[4] = {p.sa_out + grp[0], p.sb_out + grp[0], p.sa_out + grp[1], p.sb_out + grp[1]};
+                const bool w[4] = {on[0], on[0], on[1], on[1]};
+                four_scales<FMT, DT>(m, s, w, lane, left, by);
+            }
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) {
-            float w, aw;
-            weight<ACT, DT, true>(a[j], w, aw);
-            const float phi = a[j] * w;
-            da[j] = dz[j] * b[j] * (w + aw);
-            db[j] = dz[j] * phi;
-            z[j] = phi * b[j];
+            for (int i = 0; i < kAhead; ++i) {
+                if (!on[i]) break;
+                float a[kEl], b[kEl], z[kEl];
+                ra[i].get(a);
+                rb[i].get(b);
+#pragma unroll
+                for (int j = 0; j < kEl; ++j) {
+                    float w, aw;
+                    weight<ACT, DT, false>(a[j], w, aw);
+                    z[j] = a[j] * w * b[j];
+                }
+                store8<DT, VEC>(pz + out[i], lane, left, z);
+                if constexpr (FMT != kNoCodes && VEC) {
+                    encode8<FMT>(a, by[2 * i], p.qa_out + out[i], lane, left);
+                    encode8<FMT>(b, by[2 * i + 1], p.qb_out + out[i], lane, left);
+                } else if constexpr (FMT != kNoCodes) {
+                    uint32_t m[2];
+                    group_amax<VEC>(a, m);
+                    quantise8<FMT, VEC>(a, m, p.qa_out + out[i], p.sa_out + grp[i], lane, left);
+                    group_amax<VEC>(b, m);
+                    quantise8<FMT, VEC>(b, m, p.qb_out + out[i], p.sb_out + grp[i], lane, left);
+                }
+            }
+            in.advance(kAhead);
+            out.advance(kAhead);
+            grp.advance(kAhead);
         }
-        store8<DT, VEC>(static_cast<T*>(p.da) + k.row * p.ld_grad + c0, lane, left, da);
-        store8<DT, VEC>(static_cast<T*>(p.db) + k.row * p.ld_grad + c0, lane, left, db);
-        if (p.z) store8<DT, VEC>(static_cast<T*>(p.z) + at, lane, left, z);
-    }
+    });
 }
 
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) store_kernel(const Check8 p) {
+template <int DT, bool VEC, int ACT, int FMT>
+__global__ void __launch_bounds__(256, kBlocks) gated_bwd(const Gated p, const Strip t) {
+    constexpr int kAhead = VEC ? kVecAhead : 1;
+    using T = typename Storage<DT>::T;
+    constexpr bool CODES = FMT != kNoCodes;
+    const int lane = threadIdx.x & 31;
+    const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
+    for_strips(t, p.cols, [&](int64_t row0, int64_t c0, int left) {
+        Down in(row0, p.ld, c0, t.lanes), out(row0, p.cols, c0, t.lanes);
+        Down grad(row0, p.ld_grad, c0, t.lanes), grp(row0, groups, c0 / kQGroup, t.lanes);
+        const T *pa = static_cast<const T*>(p.a), *pb = static_cast<const T*>(p.b);
+        const T* pdz = static_cast<const T*>(p.dz);
+        T *pda = static_cast<T*>(p.da), *pdb = static_cast<T*>(p.db), *pz = static_cast<T*>(p.z);
+        for (int64_t rows = p.rows - row0; rows > 0; rows -= kAhead * t.lanes) {
+            Raw<DT, VEC> rz[kAhead], ra[CODES ? 1 : kAhead], rb[CODES ? 1 : kAhead];
+            Codes<VEC> ca[CODES ? kAhead : 1], cb[CODES ? kAhead : 1];
+            float fa[CODES ? kAhead : 1][2], fb[CODES ? kAhead : 1][2];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int here = rows > i * t.lanes ? left : 0;
+                rz[i].load(pdz + out[i], lane, here);
+                if constexpr (CODES) {
+                    ca[i].load(p.qa + out[i], lane, here);
+                    cb[i].load(p.qb + out[i], lane, here);
+                    load_scales<VEC>(p.sa + grp[i], lane, here, fa[i]);
+                    load_scales<VEC>(p.sb + grp[i], lane, here, fb[i]);
+                } else {
+                    ra[i].load(pa + in[i], lane, here);
+                    rb[i].load(pb + in[i], lane, here);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (rows <= i * t.lanes) break;
+                float a[kEl], b[kEl], dz[kEl], z[kEl];
+                if constexpr (CODES) {
+                    ca[i].template get<FMT>(fa[i], a);
+                    cb[i].template get<FMT>(fb[i], b);
+                } else {
+                    ra[i].get(a);
+                    rb[i].get(b);
+                }
+                rz[i].get(dz);
+#pragma unroll
+                for (int j = 0; j < kEl; ++j) {
+                    float w, aw;
+                    weight<ACT, DT, true>(a[j], w, aw);
+                    const float phi = a[j] * w;
+                    z[j] = phi * b[j];
+                    a[j] = dz[j] * b[j] * (w + aw);
+                    b[j] = dz[j] * phi;
+                }
+                store8<DT, VEC>(pda + grad[i], lane, left, a);
+                store8<DT, VEC>(pdb + grad[i], lane, left, b);
+                if (p.z) store8<DT, VEC>(pz + out[i], lane, left, z);
+            }
+            out.advance(kAhead);
+            grad.advance(kAhead);
+            if constexpr (CODES) grp.advance(kAhead);
+            else in.advance(kAhead);
+        }
+    });
+}
+
+constexpr int kCheckAhead = 4;
+
+template <int DT, bool VEC, int FMT>
+__global__ void __launch_bounds__(256, kBlocks) store_kernel(const Check8 p, const Strip t) {
     using T = typename Storage<DT>::T;
     const int lane = threadIdx.x & 31;
     const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
-    for (Walk k(p.cols); k.row < p.rows; k.next()) {
-        const int64_t c0 = (int64_t)k.seg * kSeg;
-        const int left = (int)min(p.cols - c0, (int64_t)kSeg);
-        Raw<DT, VEC> r;
-        r.load(static_cast<const T*>(p.x) + k.row * p.ld + c0, lane, left);
-        float x[kEl];
-        r.get(x);
-        quantise8<VEC>(p.format, x, p.q + k.row * p.cols + c0, p.scale + k.row * groups, c0, lane, left);
-    }
+    for_strips(t, p.cols, [&](int64_t row0, int64_t c0, int left) {
+        Down in(row0, p.ld, c0, t.lanes), out(row0, p.cols, c0, t.lanes);
+        Down grp(row0, groups, c0 / kQGroup, t.lanes);
+        const T* px = static_cast<const T*>(p.x);
+        for (int64_t rows = p.rows - row0; rows > 0; rows -= kCheckAhead * t.lanes) {
+            Raw<DT, VEC> raw[kCheckAhead];
+            bool on[kCheckAhead];
+#pragma unroll
+            for (int i = 0; i < kCheckAhead; ++i) {
+                on[i] = rows > i * t.lanes;
+                raw[i].load(px + in[i], lane, on[i] ? left : 0);
+            }
+            float by[kCheckAhead];
+            if constexpr (VEC) {
+                const uint32_t m[4] = {raw_amax(raw[0]), raw_amax(raw[1]), raw_amax(raw[2]), raw_amax(raw[3])};
+                float* const s[4] = {p.scale + grp[0], p.scale + grp[1], p.scale + grp[2], p.scale + grp[3]};
+                four_scales<FMT, DT>(m, s, on, lane, left, by);
+            }
+#pragma unroll
+            for (int i = 0; i < kCheckAhead; ++i) {
+                if (!on[i]) break;
+                float x[kEl];
+                raw[i].get(x);
+                if constexpr (VEC) {
+                    encode8<FMT>(x, by[i], p.q + out[i], lane, left);
+                } else {
+                    uint32_t m[2];
+                    group_amax<VEC>(x, m);
+                    quantise8<FMT, VEC>(x, m, p.q + out[i], p.scale + grp[i], lane, left);
+                }
+            }
+            in.advance(kCheckAhead);
+            out.advance(kCheckAhead);
+            grp.advance(kCheckAhead);
+        }
+    });
 }
 
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) load_kernel(const Check8 p) {
+template <int DT, bool VEC, int FMT>
+__global__ void __launch_bounds__(256, kBlocks) load_kernel(const Check8 p, const Strip t) {
     using T = typename Storage<DT>::T;
     const int lane = threadIdx.x & 31;
     const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
-    for (Walk k(p.cols); k.row < p.rows; k.next()) {
-        const int64_t c0 = (int64_t)k.seg * kSeg;
-        const int left = (int)min(p.cols - c0, (int64_t)kSeg);
-        Codes<VEC> q;
-        float s[2], x[kEl], ga[kEl], be[kEl];
-        q.load(p.q + k.row * p.cols + c0, lane, left);
-        load_scales<VEC>(p.scale + k.row * groups, c0, lane, left, s);
-        q.get(p.format, s, x);
+    for_strips(t, p.cols, [&](int64_t row0, int64_t c0, int left) {
+        float ga[kEl], be[kEl];
         load_param<VEC>(p.gamma, c0, lane, left, 1.f, ga);
         load_param<VEC>(p.beta, c0, lane, left, 0.f, be);
+        Down in(row0, p.cols, c0, t.lanes), out(row0, p.ld, c0, t.lanes);
+        Down grp(row0, groups, c0 / kQGroup, t.lanes);
+        T* py = static_cast<T*>(p.y);
+        for (int64_t rows = p.rows - row0; rows > 0; rows -= kCheckAhead * t.lanes) {
+            Codes<VEC> c[kCheckAhead];
+            float f[kCheckAhead][2];
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) x[j] = fmaf(ga[j], x[j], be[j]);
-        store8<DT, VEC>(static_cast<T*>(p.y) + k.row * p.ld + c0, lane, left, x);
-    }
+            for (int i = 0; i < kCheckAhead; ++i) {
+                const int here = rows > i * t.lanes ? left : 0;
+                c[i].load(p.q + in[i], lane, here);
+                load_scales<VEC>(p.scale + grp[i], lane, here, f[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kCheckAhead; ++i) {
+                if (rows <= i * t.lanes) break;
+                float x[kEl];
+                c[i].template get<FMT>(f[i], x);
+#pragma unroll
+                for (int j = 0; j < kEl; ++j) x[j] = fmaf(ga[j], x[j], be[j]);
+                store8<DT, VEC>(py + out[i], lane, left, x);
+            }
+            in.advance(kCheckAhead);
+            out.advance(kCheckAhead);
+            grp.advance(kCheckAhead);
+        }
+    });
 }
 
-// Blocks of 8 warps: as many as there are segments, at most eight waves.
-unsigned blocks(int64_t rows, int64_t cols, int sms) {
-    const int64_t segs = (cols + kSeg - 1) / kSeg;
-    const int64_t most = (int64_t)sms * 64;
-    if (rows >= most * 8 / segs + 1) return (unsigned)most;
-    const int64_t need = (rows * segs + 7) / 8;
-    return (unsigned)(need < most ? need : most);
+// Strips for one wave of `warps` warps an SM, and the blocks of 8 warps.
+unsigned strips(int64_t rows, int64_t cols, int sms, int warps, Strip& t) {
+    t.segs = (int)((cols + kSeg - 1) / kSeg);
+    const int64_t all = (int64_t)sms * warps;
+    int64_t lanes = all / t.segs;
+    if (lanes > rows) lanes = rows;
+    t.lanes = (int)(lanes < 1 ? 1 : lanes);
+    const int64_t n = ((int64_t)t.segs * t.lanes + 7) / 8;
+    return (unsigned)(n < all / 8 ? n : all / 8);
+}
+
+// The launch of one operator for a storage type, alignment and format.
+struct Launch {
+    Strip t;
+    unsigned n;
+    cudaStream_t s;
+};
+
+template <int DT, bool VEC, int ACT, int FMT>
+void run_gated(const Gated& a, bool back, const Launch& l) {
+    if (back) gated_bwd<DT, VEC, ACT, FMT><<<l.n, 256, 0, l.s>>>(a, l.t);
+    else gated_fwd<DT, VEC, ACT, FMT><<<l.n, 256, 0, l.s>>>(a, l.t);
 }
 
 template <int DT, bool VEC, int ACT>
-void run_gated(const Gated& a, bool back, bool codes, unsigned n, cudaStream_t s) {
-    if (!back) gated_fwd<DT, VEC, ACT><<<n, 256, 0, s>>>(a);
-    else if (codes) gated_bwd<DT, VEC, ACT, true><<<n, 256, 0, s>>>(a);
-    else gated_bwd<DT, VEC, ACT, false><<<n, 256, 0, s>>>(a);
+void by_format(const Gated& a, int format, bool back, const Launch& l) {
+    if (format == kNoCodes) run_gated<DT, VEC, ACT, kNoCodes>(a, back, l);
+    else if (format == kE4M3) run_gated<DT, VEC, ACT, kE4M3>(a, back, l);
+    else run_gated<DT, VEC, ACT, kInt8>(a, back, l);
 }
 
 template <int DT, bool VEC>
-void by_act(const Gated& a, bool back, bool codes, unsigned n, cudaStream_t s) {
-    if (a.act == kSilu) run_gated<DT, VEC, kSilu>(a, back, codes, n, s);
-    else if (a.act == kGelu) run_gated<DT, VEC, kGelu>(a, back, codes, n, s);
-    else run_gated<DT, VEC, kGeluTanh>(a, back, codes, n, s);
+void by_act(const Gated& a, int format, bool back, const Launch& l) {
+    if (a.act == kSilu) by_format<DT, VEC, kSilu>(a, format, back, l);
+    else if (a.act == kGelu) by_format<DT, VEC, kGelu>(a, format, back, l);
+    else by_format<DT, VEC, kGeluTanh>(a, format, back, l);
 }
 
 template <int DT>
-void by_vec(const Gated& a, bool vec, bool back, bool codes, unsigned n, cudaStream_t s) {
-    if (vec) by_act<DT, true>(a, back, codes, n, s);
-    else by_act<DT, false>(a, back, codes, n, s);
+void by_vec(const Gated& a, bool vec, int format, bool back, const Launch& l) {
+    if (vec) by_act<DT, true>(a, format, back, l);
+    else by_act<DT, false>(a, format, back, l);
 }
 
 cudaError_t run(const Gated& a, int dtype, bool back, bool codes, cudaStream_t s, int sms) {
     if (a.rows == 0) return cudaSuccess;
-    const bool strides = (codes || a.ld % kEl == 0) && (!back || a.ld_grad % kEl == 0);
+    const bool strides = (!a.a || a.ld % kEl == 0) && (!back || a.ld_grad % kEl == 0);
     const bool vec = a.cols % kEl == 0 && strides && on16(a.a) && on16(a.b) && on16(a.qa) &&
                      on16(a.qb) && on16(a.qa_out) && on16(a.qb_out) && on16(a.dz) && on16(a.z) &&
                      on16(a.da) && on16(a.db);
-    const unsigned n = blocks(a.rows, a.cols, sms);
-    if (dtype == kF32) by_vec<kF32>(a, vec, back, codes, n, s);
-    else if (dtype == kBF16) by_vec<kBF16>(a, vec, back, codes, n, s);
-    else by_vec<kF16>(a, vec, back, codes, n, s);
+    Launch l;
+    l.n = strips(a.rows, a.cols, sms, 8 * kBlocks, l.t);
+    l.s = s;
+    const int format = codes ? a.format : kNoCodes;
+    if (dtype == kF32) by_vec<kF32>(a, vec, format, back, l);
+    else if (dtype == kBF16) by_vec<kBF16>(a, vec, format, back, l);
+    else by_vec<kF16>(a, vec, format, back, l);
     count_launches(1);
     return cudaGetLastError();
 }
 
+template <int DT, bool VEC, int FMT>
+void run_check8(const Check8& a, bool load, const Launch& l) {
+    if (load) load_kernel<DT, VEC, FMT><<<l.n, 256, 0, l.s>>>(a, l.t);
+    else store_kernel<DT, VEC, FMT><<<l.n, 256, 0, l.s>>>(a, l.t);
+}
+
 template <int DT>
-void run_check8(const Check8& a, bool load, bool vec, unsigned n, cudaStream_t s) {
-    if (load) {
-        if (vec) load_kernel<DT, true><<<n, 256, 0, s>>>(a);
-        else load_kernel<DT, false><<<n, 256, 0, s>>>(a);
+void by_format(const Check8& a, bool vec, bool load, const Launch& l) {
+    if (a.format == kE4M3) {
+        if (vec) run_check8<DT, true, kE4M3>(a, load, l);
+        else run_check8<DT, false, kE4M3>(a, load, l);
     } else {
-        if (vec) store_kernel<DT, true><<<n, 256, 0, s>>>(a);
-        else store_kernel<DT, false><<<n, 256, 0, s>>>(a);
+        if (vec) run_check8<DT, true, kInt8>(a, load, l);
+        else run_check8<DT, false, kInt8>(a, load, l);
     }
 }
 
 cudaError_t check8(const Check8& a, int dtype, bool load, cudaStream_t s, int sms) {
     if (a.rows == 0) return cudaSuccess;
     const bool vec = a.cols % kEl == 0 && a.ld % kEl == 0 && on16(a.x) && on16(a.y) && on16(a.q);
-    const unsigned n = blocks(a.rows, a.cols, sms);
-    if (dtype == kF32) run_check8<kF32>(a, load, vec, n, s);
-    else if (dtype == kBF16) run_check8<kBF16>(a, load, vec, n, s);
-    else run_check8<kF16>(a, load, vec, n, s);
+    Launch l;
+    l.n = strips(a.rows, a.cols, sms, 8 * kBlocks, l.t);
+    l.s = s;
+    if (dtype == kF32) by_format<kF32>(a, vec, load, l);
+    else if (dtype == kBF16) by_format<kBF16>(a, vec, load, l);
+    else by_format<kF16>(a, vec, load, l);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -248,7 +392,7 @@ cudaError_t check8(const Check8& a, int dtype, bool load, cudaStream_t s, int sm
 }  // namespace
 
 cudaError_t gated_forward(const Gated& a, int dtype, cudaStream_t s, int sms) {
-    return run(a, dtype, false, false, s, sms);
+    return run(a, dtype, false, a.qa_out != nullptr, s, sms);
 }
 cudaError_t gated_backward(const Gated& a, int dtype, bool codes, cudaStream_t s, int sms) {
     return run(a, dtype, true, codes, s, sms);

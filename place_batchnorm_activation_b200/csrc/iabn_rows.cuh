@@ -173,11 +173,13 @@ template <> struct Q8<kInt8> {
     static constexpr float kMax = 127.f;
     // |v| <= 127: adding 1.5 * 2^23 leaves round-to-nearest-even(v) in the low
     // byte (two's complement).
-    static __device__ __forceinline__ uint32_t encode1(float v) {
-        return __float_as_uint(__fadd_rn(v, 12582912.f)) & 0xffu;
+    static __device__ __forceinline__ uint32_t round1(float v) {
+        return __float_as_uint(__fadd_rn(v, 12582912.f));
     }
     static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-        return encode1(a) | encode1(b) << 8 | encode1(c) << 16 | encode1(d) << 24;
+        const uint32_t lo = __byte_perm(round1(a), round1(b), 0x0040);
+        const uint32_t hi = __byte_perm(round1(c), round1(d), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
     }
     static __device__ __forceinline__ void decode4(uint32_t w, float* f) {
 #pragma unroll
@@ -229,17 +231,15 @@ struct Codes {
     }
 };
 
-// A lane's two scales of the segment that starts at column col0 (a multiple
-// of kSeg) of a row whose scales are at `s`.
+// A lane's two scales of the segment whose first one is at `s`.
 template <bool VEC>
-__device__ __forceinline__ void load_scales(const float* s, int64_t col0, int lane, int left,
+__device__ __forceinline__ void load_scales(const float* s, int lane, int left,
                                             float (&scale)[2]) {
-    const float* p = s + col0 / kQGroup;
     if (VEC) {
-        scale[0] = scale[1] = lane * kEl < left ? __ldg(p + lane / 16) : 0.f;
+        scale[0] = scale[1] = lane * kEl < left ? __ldg(s + (lane >> 4)) : 0.f;
     } else {
-        scale[0] = __ldg(p);
-        scale[1] = left > kQGroup ? __ldg(p + 1) : 0.f;
+        scale[0] = left > 0 ? __ldg(s) : 0.f;
+        scale[1] = left > kQGroup ? __ldg(s + 1) : 0.f;
     }
 }
 
@@ -258,29 +258,107 @@ __device__ __forceinline__ void group_scale(uint32_t bits, float& scale, float& 
     }
 }
 
-// Quantises a segment and writes its codes and scales.  All lanes of the warp
-// call it, with zeros past the row's end.
-template <int FMT, bool VEC>
-__device__ __forceinline__ void quantise8(const float (&f)[kEl], uint8_t* q, float* s,
-                                          int64_t col0, int lane, int left) {
-    uint32_t m[2] = {0, 0};
+// The largest magnitude, as bits, of the groups that a lane's elements are in:
+// m[0] under VEC (the lane's group), else m[0] and m[1] (of elements 0-3 and
+// 4-7).  All lanes of the warp call it.
+template <bool VEC>
+__device__ __forceinline__ void group_amax(const float (&f)[kEl], uint32_t (&m)[2]) {
+    m[0] = m[1] = 0;
 #pragma unroll
     for (int j = 0; j < kEl; ++j)
         m[j / 4] = max(m[j / 4], __float_as_uint(f[j]) & 0x7fffffffu);
-    float scale[2], by[2];
     if (VEC) {
-        uint32_t a = max(m[0], m[1]);
+        m[0] = max(m[0], m[1]);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        group_scale<FMT>(a, scale[0], by[0]);
-        by[1] = by[0];
-        if ((lane & 15) == 0 && lane * kEl < left) s[col0 / kQGroup + lane / 16] = scale[0];
+        for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
     } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) group_scale<FMT>(__reduce_max_sync(0xffffffffu, m[i]), scale[i], by[i]);
+        for (int i = 0; i < 2; ++i) m[i] = __reduce_max_sync(0xffffffffu, m[i]);
+    }
+}
+
+// A lane's own largest magnitude (VEC), as fp32 bits for fp32 and as the 16
+// bits of the storage type otherwise, from elements as they were loaded.
+template <int DT>
+__device__ __forceinline__ uint32_t raw_amax(const Raw<DT, true>& r) {
+    if constexpr (DT == kF32) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = r.v[i];
+            a = max(max(a, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu)),
+                    max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+        }
+        return a;
+    } else {
+        constexpr uint32_t k = 0x7fff7fffu;
+        const uint32_t a = __vmaxu2(__vmaxu2(r.v[0].x & k, r.v[0].y & k),
+                                    __vmaxu2(r.v[0].z & k, r.v[0].w & k));
+        return max(a & 0xffffu, a >> 16);
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m) {   // of raw_amax: as fp32 bits
+    if (DT == kF32) return m;
+    if (DT == kBF16) return m << 16;
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+}
+
+// Four groups at once (VEC): m[i] is the lane's own largest magnitude in group
+// i of its half-warp.  The sixteen lanes halve the number of groups that each
+// carries while they reduce, so that four reductions cost five exchanges, and
+// the four divisions one.  Writes the scales (at s[i], of the segment, where
+// on[i]) and returns every group's multiplier.
+template <int FMT, int DT>
+__device__ __forceinline__ void four_scales(const uint32_t (&m)[4], float* const (&s)[4],
+                                            const bool (&on)[4], int lane, int left,
+                                            float (&by)[4]) {
+    const bool hi = lane & 8, odd = lane & 4;
+    uint32_t a = hi ? m[2] : m[0], b = hi ? m[3] : m[1];
+    a = max(a, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 8));
+    b = max(b, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 8));
+    const uint32_t give = odd ? a : b;
+    a = max(odd ? b : a, __shfl_xor_sync(0xffffffffu, give, 4));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    float scale, mine;
+    group_scale<FMT>(amax_bits<DT>(a), scale, mine);
+    float* p = hi ? (odd ? s[3] : s[2]) : (odd ? s[1] : s[0]);
+    const bool w = hi ? (odd ? on[3] : on[2]) : (odd ? on[1] : on[0]);
+    if ((lane & 3) == 0 && w && (lane & 16) * kEl < left) p[lane >> 4] = scale;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        by[i] = __shfl_sync(0xffffffffu, mine, (lane & 16) | i << 2);
+}
+
+// A lane's eight codes with their group's multiplier.
+template <int FMT>
+__device__ __forceinline__ void encode8(const float (&f)[kEl], float by, uint8_t* q, int lane,
+                                        int left) {
+    float t[kEl];
+#pragma unroll
+    for (int j = 0; j < kEl; ++j) t[j] = __fmul_rn(f[j], by);
+    Codes<true> c;
+    c.v = make_uint2(Q8<FMT>::encode4(t[0], t[1], t[2], t[3]),
+                     Q8<FMT>::encode4(t[4], t[5], t[6], t[7]));
+    c.store(q, lane, left);
+}
+
+// Quantises a segment with its group_amax and writes its codes (at `q`) and
+// scales (at `s`, the segment's first).  Past the row's end f is zero.
+template <int FMT, bool VEC>
+__device__ __forceinline__ void quantise8(const float (&f)[kEl], const uint32_t (&m)[2],
+                                          uint8_t* q, float* s, int lane, int left) {
+    float scale[2], by[2];
+    group_scale<FMT>(m[0], scale[0], by[0]);
+    if (VEC) {
+        by[1] = by[0];
+        if ((lane & 15) == 0 && lane * kEl < left) s[lane >> 4] = scale[0];
+    } else {
+        group_scale<FMT>(m[1], scale[1], by[1]);
         if (lane == 0) {
-            s[col0 / kQGroup] = scale[0];
-            if (left > kQGroup) s[col0 / kQGroup + 1] = scale[1];
+            s[0] = scale[0];
+            if (left > kQGroup) s[1] = scale[1];
         }
     }
     float t[kEl];
@@ -293,10 +371,10 @@ __device__ __forceinline__ void quantise8(const float (&f)[kEl], uint8_t* q, flo
 }
 
 template <bool VEC>
-__device__ __forceinline__ void quantise8(int fmt, const float (&f)[kEl], uint8_t* q, float* s,
-                                          int64_t col0, int lane, int left) {
-    if (fmt == kE4M3) quantise8<kE4M3, VEC>(f, q, s, col0, lane, left);
-    else quantise8<kInt8, VEC>(f, q, s, col0, lane, left);
+__device__ __forceinline__ void quantise8(int fmt, const float (&f)[kEl], const uint32_t (&m)[2],
+                                          uint8_t* q, float* s, int lane, int left) {
+    if (fmt == kE4M3) quantise8<kE4M3, VEC>(f, m, q, s, lane, left);
+    else quantise8<kInt8, VEC>(f, m, q, s, lane, left);
 }
 
 // ---------------------------------------------------------- sums over a row
