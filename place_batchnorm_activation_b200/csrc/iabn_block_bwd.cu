@@ -35,29 +35,23 @@ __host__ __device__ inline Span worker_rows(int64_t w, int64_t rows, int64_t wor
 template <int DT, bool VEC, int V, bool CODES, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row_warps) {
     using T = typename Storage<DT>::T;
-    extern __shared__ float2 shared[];   // sums of a row, then (several rows a CTA) of columns
+    extern __shared__ float4 shared[];   // sums of a row, then (several rows a CTA) of columns
     const int warp = threadIdx.x >> 5;
-    const int y = warp / row_warps;
     const int lanes_y = (blockDim.x >> 5) / row_warps;
-    RowWarps rw;
-    rw.n = row_warps;
-    rw.w = warp - y * row_warps;
-    rw.lane = threadIdx.x & 31;
-    rw.bar = 1 + y;
-    rw.red = shared + y * 2 * row_warps;
-    rw.half = 0;
-    float* columns = reinterpret_cast<float*>(shared + 2 * (blockDim.x >> 5));
+    RowWarps<32> rw(row_warps, reinterpret_cast<float*>(shared));
+    const int y = rw.bar - 1;
+    float* columns = reinterpret_cast<float*>(shared) + lanes_y * kRowFloats;
     const float inv_n = 1.f / (float)p.cols;
     const int64_t D = p.cols;
     const int64_t slots = block_bwd_slots(p.workers, p.gates);
-    float A[V][kEl], B[V][kEl], C[V][kEl], E[V][kEl];
+    Lane8 A[V], B[V], C[V], E[V];
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) A[k][j] = B[k][j] = C[k][j] = E[k][j] = 0.f;
+        for (int j = 0; j < kEl / 2; ++j) A[k][j] = B[k][j] = C[k][j] = E[k][j] = both(0.f);
 
     // Adds the CTA's row lanes and writes a partial-sum row.
-    auto flush = [&](float (&s)[V][kEl], float* out) {
+    auto flush = [&](Lane8 (&s)[V], float* out) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
@@ -65,37 +59,38 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
                 __syncthreads();
                 float* mine = columns + warp * kSeg;
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) mine[rw.lane + 32 * j] = s[k][j];
+                for (int j = 0; j < kEl; ++j) mine[rw.lane + 32 * j] = el(s[k], j);
                 __syncthreads();
                 if (y == 0)
                     for (int o = 1; o < lanes_y; ++o) {
                         const float* other = columns + (o * rw.n + rw.w) * kSeg;
 #pragma unroll
-                        for (int j = 0; j < kEl; ++j) s[k][j] += other[rw.lane + 32 * j];
+                        for (int j = 0; j < kEl; ++j) el(s[k], j) += other[rw.lane + 32 * j];
                     }
             }
             if (y == 0) {
 #pragma unroll
                 for (int j = 0; j < kEl; ++j) {
                     const int c = seg_col<VEC>(rw.lane, j);
-                    if (c < left) out[c0 + c] = s[k][j];
+                    if (c < left) out[c0 + c] = el(s[k], j);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kEl; ++j) s[k][j] = 0.f;
+            for (int j = 0; j < kEl / 2; ++j) s[k][j] = both(0.f);
         }
     };
 
     // The normalised segment k of a row: from codes, or from the kept tensor.
     auto hat = [&](const void* src, const float* scales, const float* means, const float* rstds,
-                   int64_t row, int k, float (&f)[kEl]) {
+                   int64_t row, int k, Lane8& f) {
         const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
         if (CODES) {
             Codes<VEC> c;
             float sc[2] = {0.f, 0.f};
             c.load(static_cast<const uint8_t*>(src) + row * D + c0, rw.lane, left);
             load_scales<VEC>(scales + row * p.groups + c0 / kQGroup, rw.lane, left, sc);
-            c.get(p.format, sc, f);
+            if (p.format == kE4M3) c.template get<kE4M3>(sc, f);
+            else c.template get<kInt8>(sc, f);
         } else {
             Raw<DT, VEC> r;
             r.load(static_cast<const T*>(src) + row * D + c0, rw.lane, left);
@@ -104,7 +99,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
             const float rstd = rstds ? __ldg(rstds + row) : 1.f;
 #pragma unroll
             for (int j = 0; j < kEl; ++j)
-                f[j] = seg_col<VEC>(rw.lane, j) < left ? (f[j] - mean) * rstd : 0.f;
+                el(f, j) = seg_col<VEC>(rw.lane, j) < left ? (el(f, j) - mean) * rstd : 0.f;
         }
     };
 
@@ -115,7 +110,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
         const int64_t hi = end < mine.hi ? end : mine.hi;
         const float* gate = p.gate ? p.gate + gr * D : nullptr;
         for (int64_t row = lo + y; row < hi; row += lanes_y) {
-            float t[V][kEl];
+            Lane8 t[V];
             if (p.dh_out) {
                 Raw<DT, VEC> r[V];
 #pragma unroll
@@ -129,11 +124,11 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
 #pragma unroll
                 for (int k = 0; k < V; ++k)
 #pragma unroll
-                    for (int j = 0; j < kEl; ++j) t[k][j] = 0.f;
+                    for (int j = 0; j < kEl / 2; ++j) t[k][j] = both(0.f);
             }
             if (p.pre != kNormNone) {
-                float g[V][kEl], x[V][kEl];
-                float s = 0.f, sx = 0.f;
+                Lane8 g[V], x[V];
+                float2 s = both(0.f), sx = both(0.f);
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
@@ -141,15 +136,15 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
                     r.load(static_cast<const T*>(p.dn) + row * D + c0, rw.lane, left);
                     hat(p.sh, p.scale_pre, p.mean_pre, p.rstd_pre, row, k, x[k]);
                     r.get(g[k]);
-                    float ga[kEl];
+                    Lane8 ga;
                     load_param<VEC>(p.gamma_pre, c0, rw.lane, left, 1.f, ga);
 #pragma unroll
-                    for (int j = 0; j < kEl; ++j) {
-                        C[k][j] = fmaf(g[k][j], x[k][j], C[k][j]);
-                        E[k][j] += g[k][j];
-                        g[k][j] *= ga[j];
-                        s += g[k][j];
-                        sx = fmaf(g[k][j], x[k][j], sx);
+                    for (int j = 0; j < kEl / 2; ++j) {
+                        C[k][j] = fma2(g[k][j], x[k][j], C[k][j]);
+                        E[k][j] = add2(E[k][j], g[k][j]);
+                        g[k][j] = mul2(g[k][j], ga[j]);
+                        s = add2(s, g[k][j]);
+                        sx = fma2(g[k][j], x[k][j], sx);
                     }
                 }
                 const float2 m = rw.sum(s, sx);
@@ -160,13 +155,13 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
                     const int left = p.cols - (k * rw.n + rw.w) * kSeg;
 #pragma unroll
                     for (int j = 0; j < kEl; ++j) {
-                        const float d = fmaf(-slope, x[k][j], g[k][j] - level);
-                        if (seg_col<VEC>(rw.lane, j) < left) t[k][j] = fmaf(rstd, d, t[k][j]);
+                        const float d = fmaf(-slope, el(x[k], j), el(g[k], j) - level);
+                        if (seg_col<VEC>(rw.lane, j) < left) el(t[k], j) = fmaf(rstd, d, el(t[k], j));
                     }
                 }
             }
-            float x[V][kEl];
-            float s = 0.f, sx = 0.f;
+            Lane8 x[V];
+            float2 s = both(0.f), sx = both(0.f);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
@@ -174,23 +169,23 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
                     hat(p.su, p.scale_post, p.mean_post, p.rstd_post, row, k, x[k]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kEl; ++j) x[k][j] = 0.f;
+                    for (int j = 0; j < kEl / 2; ++j) x[k][j] = both(0.f);
                 }
                 // (all inputs of this column have been read: dh may be any of them)
-                float o[kEl];
+                Lane8 o;
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) o[j] = p.alpha * t[k][j];
+                for (int j = 0; j < kEl / 2; ++j) o[j] = mul2(both(p.alpha), t[k][j]);
                 store8<DT, VEC>(static_cast<T*>(p.dh) + row * D + c0, rw.lane, left, o);
-                float ga[kEl], gt[kEl];
+                Lane8 ga, gt;
                 load_param<VEC>(p.gamma_post, c0, rw.lane, left, 1.f, ga);
                 load_param<VEC>(gate, c0, rw.lane, left, 1.f, gt);
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) {
-                    A[k][j] = fmaf(t[k][j], x[k][j], A[k][j]);
-                    B[k][j] += t[k][j];
-                    t[k][j] *= gt[j] * ga[j];
-                    s += t[k][j];
-                    sx = fmaf(t[k][j], x[k][j], sx);
+                for (int j = 0; j < kEl / 2; ++j) {
+                    A[k][j] = fma2(t[k][j], x[k][j], A[k][j]);
+                    B[k][j] = add2(B[k][j], t[k][j]);
+                    t[k][j] = mul2(t[k][j], mul2(gt[j], ga[j]));
+                    s = add2(s, t[k][j]);
+                    sx = fma2(t[k][j], x[k][j], sx);
                 }
             }
             if (!p.du) continue;
@@ -202,7 +197,7 @@ __global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row
                 for (int k = 0; k < V; ++k)
 #pragma unroll
                     for (int j = 0; j < kEl; ++j)
-                        t[k][j] = rstd * fmaf(-slope, x[k][j], t[k][j] - level);
+                        el(t[k], j) = rstd * fmaf(-slope, el(x[k], j), el(t[k], j) - level);
             }
 #pragma unroll
             for (int k = 0; k < V; ++k) {
@@ -304,7 +299,7 @@ __global__ void __launch_bounds__(1024) block_bwd_columns(const BlockBwd p) {
 template <int DT, bool VEC, bool CODES, int V, int MAXT>
 cudaError_t launch(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
     const int threads = 32 * row_warps * rows_cta;
-    const size_t smem = (threads / 32) * (2 * sizeof(float2) + (rows_cta > 1 ? kSeg * sizeof(float) : 0));
+    const size_t smem = (rows_cta * kRowFloats + (rows_cta > 1 ? threads / 32 * kSeg : 0)) * sizeof(float);
     block_bwd_rows<DT, VEC, V, CODES, MAXT><<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
     count_launches(1);
     return cudaGetLastError();

@@ -12,7 +12,7 @@ namespace iabn {
 constexpr int kQGroup = 128;
 
 enum : int { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
-enum : int { kE4M3 = 0, kInt8 = 1 };
+enum : int { kNoCodes = -1, kE4M3 = 0, kInt8 = 1 };
 enum : int { kSilu = 0, kGelu = 1, kGeluTanh = 2 };
 
 inline int64_t q_groups(int64_t cols) { return (cols + kQGroup - 1) / kQGroup; }

@@ -28,30 +28,44 @@ __device__ __forceinline__ float fast_inverse(float x) {
     return y;
 }
 template <int DT>
-__device__ __forceinline__ float exp_of(float x) {
-    return DT == kF32 ? expf(x) : fast_exp2(x * 1.4426950408889634f);
+__device__ __forceinline__ float2 exp_of(float2 x) {
+    if (DT == kF32) return make_float2(expf(x.x), expf(x.y));
+    x = mul2(x, both(1.4426950408889634f));
+    return make_float2(fast_exp2(x.x), fast_exp2(x.y));
 }
 template <int DT>
 __device__ __forceinline__ float inverse(float x) {   // of 1 + e^y: in [1, inf]
     return DT == kF32 ? 1.f / x : fast_inverse(x);
 }
 
-// w(a), and a w'(a) where SLOPE.
+// w(a), and a w'(a) where SLOPE, of two values.
 template <int ACT, int DT, bool SLOPE>
-__device__ __forceinline__ void weight(float a, float& w, float& aw) {
-    if (ACT == kSilu) {
-        w = inverse<DT>(1.f + exp_of<DT>(-a));
-        if (SLOPE) aw = a * w * (1.f - w);
-    } else if (ACT == kGelu) {
-        w = 0.5f * erfcf(a * -0.70710678118654752f);
-        if (SLOPE) aw = a * 0.39894228040143268f * exp_of<DT>(-0.5f * a * a);
+__device__ __forceinline__ void weight2(float2 a, float2& w, float2& aw) {
+    if constexpr (ACT == kSilu || ACT == kGeluTanh) {
+        float2 y = mul2(a, both(-1.f)), c = a, q;   // w = 1/(1 + e^y)
+        if constexpr (ACT == kGeluTanh) {
+            // beyond +-32 w is 0 or 1 in fp32: the clamp keeps a^3 finite
+            c = make_float2(fminf(fmaxf(a.x, -32.f), 32.f), fminf(fmaxf(a.y, -32.f), 32.f));
+            q = mul2(mul2(c, c), both(0.044715f));
+            y = mul2(mul2(c, both(-1.5957691216057308f)), add2(q, both(1.f)));
+        }
+        const float2 d = add2(exp_of<DT>(y), both(1.f));
+        w = make_float2(inverse<DT>(d.x), inverse<DT>(d.y));
+        if (SLOPE) {
+            aw = mul2(mul2(c, w), fma2(w, both(-1.f), both(1.f)));
+            if constexpr (ACT == kGeluTanh)
+                aw = mul2(mul2(aw, both(1.5957691216057308f)), fma2(q, both(3.f), both(1.f)));
+        }
+        if constexpr (ACT == kGeluTanh) {   // the clamp loses NaN
+            if (a.x != a.x) w.x = a.x;
+            if (a.y != a.y) w.y = a.y;
+        }
     } else {
-        // beyond +-32 w is 0 or 1 in fp32: the clamp keeps a^3 finite
-        const float c = fminf(fmaxf(a, -32.f), 32.f);
-        const float q = 0.044715f * c * c;
-        w = inverse<DT>(1.f + exp_of<DT>(-1.5957691216057308f * c * (1.f + q)));
-        if (SLOPE) aw = c * w * (1.f - w) * 1.5957691216057308f * fmaf(3.f, q, 1.f);
-        if (a != a) w = a;
+        w = make_float2(0.5f * erfcf(a.x * -0.70710678118654752f),
+                        0.5f * erfcf(a.y * -0.70710678118654752f));
+        if (SLOPE)
+            aw = mul2(mul2(a, both(0.39894228040143268f)),
+                      exp_of<DT>(mul2(mul2(a, a), both(-0.5f))));
     }
 }
 
@@ -91,7 +105,6 @@ struct Down {
 // one take eight times the load instructions, so one row is ahead enough
 // (777 x 2731: 10.4 us, 13.1 with two).
 constexpr int kVecAhead = 2;
-constexpr int kNoCodes = -1;   // in place of a checkpoint format
 constexpr int kBlocks = 4;
 
 template <int DT, bool VEC, int ACT, int FMT>
@@ -117,32 +130,30 @@ __global__ void __launch_bounds__(256, kBlocks) gated_fwd(const Gated p, const S
             float by[2 * kAhead];
             if constexpr (FMT != kNoCodes && VEC) {
                 const uint32_t m[4] = {raw_amax(ra[0]), raw_amax(rb[0]), raw_amax(ra[1]), raw_amax(rb[1])};
-                float* const s[4] = {p.sa_out + grp[0], p.sb_out + grp[0], p.sa_out + grp[1], p.sb_out + grp[1]};
-                const bool w[4] = {on[0], on[0], on[1], on[1]};
-                four_scales<FMT, DT>(m, s, w, lane, left, by);
+                const float scale = group_scales<FMT, DT, 4>(m, lane, by);
+                const int i = group_carried<4>(lane);   // row i/2, a or b
+                if (group_writer<4>(lane) && (lane & 16) * kEl < left && rows > (i >> 1) * t.lanes)
+                    (i & 1 ? p.sb_out : p.sa_out)[grp[i >> 1] + (lane >> 4)] = scale;
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (!on[i]) break;
-                float a[kEl], b[kEl], z[kEl];
+                Lane8 a, b, z;
                 ra[i].get(a);
                 rb[i].get(b);
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) {
-                    float w, aw;
-                    weight<ACT, DT, false>(a[j], w, aw);
-                    z[j] = a[j] * w * b[j];
+                for (int j = 0; j < kEl / 2; ++j) {
+                    float2 w, aw;
+                    weight2<ACT, DT, false>(a[j], w, aw);
+                    z[j] = mul2(mul2(a[j], w), b[j]);
                 }
                 store8<DT, VEC>(pz + out[i], lane, left, z);
                 if constexpr (FMT != kNoCodes && VEC) {
                     encode8<FMT>(a, by[2 * i], p.qa_out + out[i], lane, left);
                     encode8<FMT>(b, by[2 * i + 1], p.qb_out + out[i], lane, left);
                 } else if constexpr (FMT != kNoCodes) {
-                    uint32_t m[2];
-                    group_amax<VEC>(a, m);
-                    quantise8<FMT, VEC>(a, m, p.qa_out + out[i], p.sa_out + grp[i], lane, left);
-                    group_amax<VEC>(b, m);
-                    quantise8<FMT, VEC>(b, m, p.qb_out + out[i], p.sb_out + grp[i], lane, left);
+                    quantise_any<FMT>(a, p.qa_out + out[i], p.sa_out + grp[i], lane, left);
+                    quantise_any<FMT>(b, p.qb_out + out[i], p.sb_out + grp[i], lane, left);
                 }
             }
             in.advance(kAhead);
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(256, kBlocks) gated_bwd(const Gated p, const S
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 if (rows <= i * t.lanes) break;
-                float a[kEl], b[kEl], dz[kEl], z[kEl];
+                Lane8 a, b, dz, z;
                 if constexpr (CODES) {
                     ca[i].template get<FMT>(fa[i], a);
                     cb[i].template get<FMT>(fb[i], b);
@@ -196,13 +207,13 @@ __global__ void __launch_bounds__(256, kBlocks) gated_bwd(const Gated p, const S
                 }
                 rz[i].get(dz);
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) {
-                    float w, aw;
-                    weight<ACT, DT, true>(a[j], w, aw);
-                    const float phi = a[j] * w;
-                    z[j] = phi * b[j];
-                    a[j] = dz[j] * b[j] * (w + aw);
-                    b[j] = dz[j] * phi;
+                for (int j = 0; j < kEl / 2; ++j) {
+                    float2 w, aw;
+                    weight2<ACT, DT, true>(a[j], w, aw);
+                    const float2 phi = mul2(a[j], w);
+                    z[j] = mul2(phi, b[j]);
+                    a[j] = mul2(mul2(dz[j], b[j]), add2(w, aw));
+                    b[j] = mul2(dz[j], phi);
                 }
                 store8<DT, VEC>(pda + grad[i], lane, left, a);
                 store8<DT, VEC>(pdb + grad[i], lane, left, b);
@@ -238,20 +249,20 @@ __global__ void __launch_bounds__(256, kBlocks) store_kernel(const Check8 p, con
             float by[kCheckAhead];
             if constexpr (VEC) {
                 const uint32_t m[4] = {raw_amax(raw[0]), raw_amax(raw[1]), raw_amax(raw[2]), raw_amax(raw[3])};
-                float* const s[4] = {p.scale + grp[0], p.scale + grp[1], p.scale + grp[2], p.scale + grp[3]};
-                four_scales<FMT, DT>(m, s, on, lane, left, by);
+                const float scale = group_scales<FMT, DT, 4>(m, lane, by);
+                const int i = group_carried<4>(lane);
+                if (group_writer<4>(lane) && (lane & 16) * kEl < left && rows > i * t.lanes)
+                    p.scale[grp[i] + (lane >> 4)] = scale;
             }
 #pragma unroll
             for (int i = 0; i < kCheckAhead; ++i) {
                 if (!on[i]) break;
-                float x[kEl];
+                Lane8 x;
                 raw[i].get(x);
                 if constexpr (VEC) {
                     encode8<FMT>(x, by[i], p.q + out[i], lane, left);
                 } else {
-                    uint32_t m[2];
-                    group_amax<VEC>(x, m);
-                    quantise8<FMT, VEC>(x, m, p.q + out[i], p.scale + grp[i], lane, left);
+                    quantise_any<FMT>(x, p.q + out[i], p.scale + grp[i], lane, left);
                 }
             }
             in.advance(kCheckAhead);
@@ -267,7 +278,7 @@ __global__ void __launch_bounds__(256, kBlocks) load_kernel(const Check8 p, cons
     const int lane = threadIdx.x & 31;
     const int64_t groups = (p.cols + kQGroup - 1) / kQGroup;
     for_strips(t, p.cols, [&](int64_t row0, int64_t c0, int left) {
-        float ga[kEl], be[kEl];
+        Lane8 ga, be;
         load_param<VEC>(p.gamma, c0, lane, left, 1.f, ga);
         load_param<VEC>(p.beta, c0, lane, left, 0.f, be);
         Down in(row0, p.cols, c0, t.lanes), out(row0, p.ld, c0, t.lanes);
@@ -285,10 +296,10 @@ __global__ void __launch_bounds__(256, kBlocks) load_kernel(const Check8 p, cons
 #pragma unroll
             for (int i = 0; i < kCheckAhead; ++i) {
                 if (rows <= i * t.lanes) break;
-                float x[kEl];
+                Lane8 x;
                 c[i].template get<FMT>(f[i], x);
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) x[j] = fmaf(ga[j], x[j], be[j]);
+                for (int j = 0; j < kEl / 2; ++j) x[j] = fma2(ga[j], x[j], be[j]);
                 store8<DT, VEC>(py + out[i], lane, left, x);
             }
             in.advance(kCheckAhead);

@@ -1,6 +1,7 @@
 // iabn_rows.cuh -- device-side building blocks of the row operators
 // (iabn_block.h): how a warp's lanes share a row, loads and stores of the
-// storage types and of 8-bit codes, the 8-bit quantiser and sums over a row.
+// storage types and of 8-bit codes, the 8-bit quantiser, sums over a row and
+// a thread's asynchronous ring.
 //
 // A warp takes a segment of 256 columns of a row, eight a lane.  Two maps:
 //   VEC   lane l holds columns 8l .. 8l+7: one 16-byte access (two for fp32)
@@ -10,6 +11,10 @@
 //         warp's accesses still being consecutive elements.
 // Either way a segment holds two checkpoint groups of 128 columns: lanes 0-15
 // and 16-31 under VEC, elements 0-3 and 4-7 of every lane otherwise.
+//
+// A lane's eight values are four float2, worked on two at a time (the f32x2
+// instructions): these kernels are bound by the instructions they issue as
+// soon as they are near the HBM rate.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -21,35 +26,75 @@ namespace iabn {
 
 constexpr int kSeg = 256;   // columns of a warp's segment
 constexpr int kEl = 8;      // of them, a lane's
+using Lane8 = float2[kEl / 2];
 
 template <bool VEC>
 __device__ __forceinline__ int seg_col(int lane, int j) {
     return VEC ? lane * kEl + j : lane + 32 * j;
 }
 
-__device__ __forceinline__ float2 unpack2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
-__device__ __forceinline__ float2 unpack2(__half2 v) { return __half22float2(v); }
+// ------------------------------------------------------ two values at a time
 
-template <class T2>
-__device__ __forceinline__ T2 pack2(float a, float b);
-template <>
-__device__ __forceinline__ __nv_bfloat162 pack2<__nv_bfloat162>(float a, float b) {
-    return __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ unsigned long long bits2(float2 v) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
 }
-template <>
-__device__ __forceinline__ __half2 pack2<__half2>(float a, float b) {
-    return __floats2half2_rn(a, b);
+__device__ __forceinline__ float2 float2_of(unsigned long long b) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+    return v;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Element j of a lane's eight.
+__device__ __forceinline__ float& el(Lane8& f, int j) { return j & 1 ? f[j / 2].y : f[j / 2].x; }
+__device__ __forceinline__ float el(const Lane8& f, int j) { return j & 1 ? f[j / 2].y : f[j / 2].x; }
+
+// ----------------------------------------------------------- loads and stores
+
 template <int DT> struct Pair { using T = __nv_bfloat162; };
 template <> struct Pair<kF16> { using T = __half2; };
+
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (DT == kBF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    if (DT == kBF16) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t*>(&t);
+    }
+    const __half2 t = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
 
 // A lane's eight elements as they were loaded (a batch of loads is in flight
 // before any is converted).
 template <int DT, bool VEC>
 struct Raw {
     using T = typename Storage<DT>::T;
+    static constexpr int kQuads = DT == kF32 ? 2 : 1;   // 16-byte accesses under VEC
     union {
-        uint4 v[DT == kF32 ? 2 : 1];
+        uint4 v[kQuads];
         T e[kEl];
     };
     __device__ __forceinline__ Raw() {}
@@ -60,8 +105,7 @@ struct Raw {
             const bool in = lane * kEl < left;
             const uint4* q = reinterpret_cast<const uint4*>(p + lane * kEl);
 #pragma unroll
-            for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i)
-                v[i] = in ? ldg_cs(q + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kQuads; ++i) v[i] = in ? ldg_cs(q + i) : make_uint4(0, 0, 0, 0);
         } else {
 #pragma unroll
             for (int j = 0; j < kEl; ++j) {
@@ -70,62 +114,73 @@ struct Raw {
             }
         }
     }
-    __device__ __forceinline__ void get(float (&f)[kEl]) const {
-        if constexpr (DT == kF32 || !VEC) {
+    __device__ __forceinline__ void get(Lane8& f) const {
+        if constexpr (DT == kF32 && VEC) {
 #pragma unroll
-            for (int j = 0; j < kEl; ++j) f[j] = Storage<DT>::load(&e[j]);
-        } else {
-            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 t = unpack2(*reinterpret_cast<const typename Pair<DT>::T*>(&w[j]));
-                f[2 * j] = t.x;
-                f[2 * j + 1] = t.y;
+            for (int i = 0; i < 2; ++i) {
+                f[2 * i] = make_float2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                f[2 * i + 1] = make_float2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
             }
+        } else if constexpr (!VEC) {
+#pragma unroll
+            for (int j = 0; j < kEl; ++j) el(f, j) = Storage<DT>::load(&e[j]);
+        } else {
+            f[0] = unpack2<DT>(v[0].x);
+            f[1] = unpack2<DT>(v[0].y);
+            f[2] = unpack2<DT>(v[0].z);
+            f[3] = unpack2<DT>(v[0].w);
         }
     }
 };
 
+// Streaming stores where `on`, likewise without a branch.
+__device__ __forceinline__ void store16_if(void* p, uint4 v, bool on) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %5, 0;\n\t"
+                 "@p st.global.cs.v4.b32 [%0], {%1, %2, %3, %4}; }" ::"l"(p), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w), "r"((int)on)
+                 : "memory");
+}
+__device__ __forceinline__ void store8_if(void* p, uint2 v, bool on) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %3, 0;\n\t"
+                 "@p st.global.cs.v2.b32 [%0], {%1, %2}; }" ::"l"(p), "r"(v.x), "r"(v.y),
+                 "r"((int)on)
+                 : "memory");
+}
+
 template <int DT, bool VEC>
 __device__ __forceinline__ void store8(typename Storage<DT>::T* p, int lane, int left,
-                                       const float (&f)[kEl]) {
+                                       const Lane8& f) {
     using T = typename Storage<DT>::T;
     if constexpr (VEC) {
-        if (lane * kEl >= left) return;
+        const bool on = lane * kEl < left;
         uint4* q = reinterpret_cast<uint4*>(p + lane * kEl);
         if constexpr (DT == kF32) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                __stcs(q + i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
-                                         __float_as_uint(f[4 * i + 2]),
-                                         __float_as_uint(f[4 * i + 3])));
+                store16_if(q + i,
+                           make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y),
+                                      __float_as_uint(f[2 * i + 1].x), __float_as_uint(f[2 * i + 1].y)),
+                           on);
         } else {
-            using P = typename Pair<DT>::T;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const P t = pack2<P>(f[2 * j], f[2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t*>(&t);
-            }
-            __stcs(q, make_uint4(w[0], w[1], w[2], w[3]));
+            store16_if(q, make_uint4(pack2<DT>(f[0]), pack2<DT>(f[1]), pack2<DT>(f[2]), pack2<DT>(f[3])), on);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < kEl; ++j) {
             const int c = lane + 32 * j;
-            if (c < left) Storage<DT>::store(reinterpret_cast<T*>(p) + c, f[j]);
+            if (c < left) Storage<DT>::store(reinterpret_cast<T*>(p) + c, el(f, j));
         }
     }
 }
 
 // Eight float32 parameters by column (gamma, beta, gate), `def` where p is
-// null or past the row's end.  Read again for every row: they stay in cache.
+// null or past the row's end.
 template <bool VEC>
 __device__ __forceinline__ void load_param(const float* p, int64_t col0, int lane, int left,
-                                           float def, float (&f)[kEl]) {
+                                           float def, Lane8& f) {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) f[j] = def;
+        for (int j = 0; j < kEl / 2; ++j) f[j] = both(def);
         return;
     }
     if (VEC && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
@@ -134,16 +189,14 @@ __device__ __forceinline__ void load_param(const float* p, int64_t col0, int lan
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float4 v = in ? __ldg(q + i) : make_float4(def, def, def, def);
-            f[4 * i] = v.x;
-            f[4 * i + 1] = v.y;
-            f[4 * i + 2] = v.z;
-            f[4 * i + 3] = v.w;
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < kEl; ++j) {
             const int c = seg_col<VEC>(lane, j);
-            f[j] = c < left ? __ldg(p + col0 + c) : def;
+            el(f, j) = c < left ? __ldg(p + col0 + c) : def;
         }
     }
 }
@@ -153,19 +206,17 @@ __device__ __forceinline__ void load_param(const float* p, int64_t col0, int lan
 template <int FMT> struct Q8;
 template <> struct Q8<kE4M3> {
     static constexpr float kMax = 448.f;
-    static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-        return lo | hi << 16;
+    static __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+        return __byte_perm(lo, hi, 0x5410);
     }
-    static __device__ __forceinline__ void decode4(uint32_t w, float* f) {
+    static __device__ __forceinline__ void decode4(uint32_t w, float2* f) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const __half2_raw r =
                 __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
-            const float2 t = __half22float2(__half2(r));
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
+            f[i] = __half22float2(__half2(r));
         }
     }
 };
@@ -173,17 +224,21 @@ template <> struct Q8<kInt8> {
     static constexpr float kMax = 127.f;
     // |v| <= 127: adding 1.5 * 2^23 leaves round-to-nearest-even(v) in the low
     // byte (two's complement).
-    static __device__ __forceinline__ uint32_t round1(float v) {
-        return __float_as_uint(__fadd_rn(v, 12582912.f));
-    }
-    static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-        const uint32_t lo = __byte_perm(round1(a), round1(b), 0x0040);
-        const uint32_t hi = __byte_perm(round1(c), round1(d), 0x0040);
+    static __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
+        a = add2(a, both(12582912.f));
+        b = add2(b, both(12582912.f));
+        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
         return __byte_perm(lo, hi, 0x5410);
     }
-    static __device__ __forceinline__ void decode4(uint32_t w, float* f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+    // The byte, its sign bit flipped, below 2^23: (2^23 + byte + 128) - (2^23 + 128).
+    static __device__ __forceinline__ void decode4(uint32_t w, float2* f) {
+        w ^= 0x80808080u;
+        const float2 base = both(-8388736.f);
+        f[0] = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
+                                __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))), base);
+        f[1] = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)),
+                                __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443))), base);
     }
 };
 
@@ -207,7 +262,7 @@ struct Codes {
     }
     __device__ __forceinline__ void store(uint8_t* p, int lane, int left) const {
         if (VEC) {
-            if (lane * kEl < left) __stcs(reinterpret_cast<uint2*>(p + lane * kEl), v);
+            store8_if(p + lane * kEl, v, lane * kEl < left);
         } else {
             const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
@@ -219,15 +274,11 @@ struct Codes {
     }
     // scale[0], scale[1]: those of elements 0-3 and 4-7.
     template <int FMT>
-    __device__ __forceinline__ void get(const float (&scale)[2], float (&f)[kEl]) const {
+    __device__ __forceinline__ void get(const float (&scale)[2], Lane8& f) const {
         Q8<FMT>::decode4(v.x, f);
-        Q8<FMT>::decode4(v.y, f + 4);
+        Q8<FMT>::decode4(v.y, f + 2);
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) f[j] *= scale[j / 4];
-    }
-    __device__ __forceinline__ void get(int fmt, const float (&scale)[2], float (&f)[kEl]) const {
-        if (fmt == kE4M3) get<kE4M3>(scale, f);
-        else get<kInt8>(scale, f);
+        for (int j = 0; j < kEl / 2; ++j) f[j] = mul2(f[j], both(scale[j / 2]));
     }
 };
 
@@ -258,42 +309,31 @@ __device__ __forceinline__ void group_scale(uint32_t bits, float& scale, float& 
     }
 }
 
-// The largest magnitude, as bits, of the groups that a lane's elements are in:
-// m[0] under VEC (the lane's group), else m[0] and m[1] (of elements 0-3 and
-// 4-7).  All lanes of the warp call it.
-template <bool VEC>
-__device__ __forceinline__ void group_amax(const float (&f)[kEl], uint32_t (&m)[2]) {
-    m[0] = m[1] = 0;
-#pragma unroll
-    for (int j = 0; j < kEl; ++j)
-        m[j / 4] = max(m[j / 4], __float_as_uint(f[j]) & 0x7fffffffu);
-    if (VEC) {
-        m[0] = max(m[0], m[1]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) m[i] = __reduce_max_sync(0xffffffffu, m[i]);
-    }
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
 }
 
-// A lane's own largest magnitude (VEC), as fp32 bits for fp32 and as the 16
-// bits of the storage type otherwise, from elements as they were loaded.
+// A lane's own largest magnitude of eight floats, as bits.
+__device__ __forceinline__ uint32_t own_amax(const Lane8& f) {
+    return __float_as_uint(amax3(amax3(f[0].x, f[0].y, f[1].x), amax3(f[1].y, f[2].x, f[2].y),
+                                 amax3(f[3].x, f[3].y, 0.f)));
+}
+
+// The same (VEC) from elements as they were loaded: as fp32 bits for fp32, as
+// the 16 bits of the storage type otherwise.
 template <int DT>
 __device__ __forceinline__ uint32_t raw_amax(const Raw<DT, true>& r) {
     if constexpr (DT == kF32) {
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = r.v[i];
-            a = max(max(a, max(v.x & 0x7fffffffu, v.y & 0x7fffffffu)),
-                    max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
-        }
-        return a;
+        Lane8 f;
+        r.get(f);
+        return own_amax(f);
     } else {
         constexpr uint32_t k = 0x7fff7fffu;
-        const uint32_t a = __vmaxu2(__vmaxu2(r.v[0].x & k, r.v[0].y & k),
-                                    __vmaxu2(r.v[0].z & k, r.v[0].w & k));
+        const uint32_t a = __vmaxu2(__vimax3_u16x2(r.v[0].x & k, r.v[0].y & k, r.v[0].z & k),
+                                    r.v[0].w & k);
         return max(a & 0xffffu, a >> 16);
     }
 }
@@ -304,111 +344,196 @@ __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {   // of raw_amax: as
     return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
 }
 
-// Four groups at once (VEC): m[i] is the lane's own largest magnitude in group
-// i of its half-warp.  The sixteen lanes halve the number of groups that each
-// carries while they reduce, so that four reductions cost five exchanges, and
-// the four divisions one.  Writes the scales (at s[i], of the segment, where
-// on[i]) and returns every group's multiplier.
-template <int FMT, int DT>
-__device__ __forceinline__ void four_scales(const uint32_t (&m)[4], float* const (&s)[4],
-                                            const bool (&on)[4], int lane, int left,
-                                            float (&by)[4]) {
+// N = 1, 2 or 4 groups at once (VEC): m[i] is the lane's own largest magnitude
+// in group i of its half-warp.  The sixteen lanes halve the number of groups
+// that each carries while they reduce, so that four reductions cost five
+// exchanges in place of sixteen, and the N divisions are one.  Returns every
+// group's multiplier and the scale of the group that this lane carries,
+// group_carried<N>.
+template <int FMT, int DT, int N>
+__device__ __forceinline__ float group_scales(const uint32_t (&m)[N], int lane, float (&by)[N]) {
     const bool hi = lane & 8, odd = lane & 4;
-    uint32_t a = hi ? m[2] : m[0], b = hi ? m[3] : m[1];
-    a = max(a, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 8));
-    b = max(b, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 8));
-    const uint32_t give = odd ? a : b;
-    a = max(odd ? b : a, __shfl_xor_sync(0xffffffffu, give, 4));
+    uint32_t a = m[0];
+    if constexpr (N == 4) {
+        a = hi ? m[2] : m[0];
+        uint32_t b = hi ? m[3] : m[1];
+        a = max(a, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 8));
+        b = max(b, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 8));
+        const uint32_t give = odd ? a : b;
+        a = max(odd ? b : a, __shfl_xor_sync(0xffffffffu, give, 4));
+    } else {
+        if constexpr (N == 2)
+            a = max(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], 8));
+        else
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
+    }
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     float scale, mine;
     group_scale<FMT>(amax_bits<DT>(a), scale, mine);
-    float* p = hi ? (odd ? s[3] : s[2]) : (odd ? s[1] : s[0]);
-    const bool w = hi ? (odd ? on[3] : on[2]) : (odd ? on[1] : on[0]);
-    if ((lane & 3) == 0 && w && (lane & 16) * kEl < left) p[lane >> 4] = scale;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        by[i] = __shfl_sync(0xffffffffu, mine, (lane & 16) | i << 2);
+    for (int i = 0; i < N; ++i)
+        by[i] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) | i * (16 / N));
+    return scale;
+}
+// Which of the N groups a lane carries, and whether it is the one to write it.
+template <int N>
+__device__ __forceinline__ int group_carried(int lane) {
+    return N == 4 ? (lane >> 2) & 3 : N == 2 ? (lane >> 3) & 1 : 0;
+}
+template <int N>
+__device__ __forceinline__ bool group_writer(int lane) {
+    return (lane & (16 / N - 1)) == 0;
 }
 
 // A lane's eight codes with their group's multiplier.
 template <int FMT>
-__device__ __forceinline__ void encode8(const float (&f)[kEl], float by, uint8_t* q, int lane,
-                                        int left) {
-    float t[kEl];
-#pragma unroll
-    for (int j = 0; j < kEl; ++j) t[j] = __fmul_rn(f[j], by);
+__device__ __forceinline__ void encode8(const Lane8& f, float by, uint8_t* q, int lane, int left) {
     Codes<true> c;
-    c.v = make_uint2(Q8<FMT>::encode4(t[0], t[1], t[2], t[3]),
-                     Q8<FMT>::encode4(t[4], t[5], t[6], t[7]));
+    c.v = make_uint2(Q8<FMT>::encode4(mul2(f[0], both(by)), mul2(f[1], both(by))),
+                     Q8<FMT>::encode4(mul2(f[2], both(by)), mul2(f[3], both(by))));
     c.store(q, lane, left);
 }
 
-// Quantises a segment with its group_amax and writes its codes (at `q`) and
-// scales (at `s`, the segment's first).  Past the row's end f is zero.
-template <int FMT, bool VEC>
-__device__ __forceinline__ void quantise8(const float (&f)[kEl], const uint32_t (&m)[2],
-                                          uint8_t* q, float* s, int lane, int left) {
+// Quantises a segment element by element (not VEC) and writes its codes (at q)
+// and scales (at s, the segment's first).  All lanes of the warp call it, with
+// zeros past the row's end.
+template <int FMT>
+__device__ __forceinline__ void quantise_any(const Lane8& f, uint8_t* q, float* s, int lane,
+                                             int left) {
     float scale[2], by[2];
-    group_scale<FMT>(m[0], scale[0], by[0]);
-    if (VEC) {
-        by[1] = by[0];
-        if ((lane & 15) == 0 && lane * kEl < left) s[lane >> 4] = scale[0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float a = amax3(amax3(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x), f[2 * i + 1].y, 0.f);
+        group_scale<FMT>(__reduce_max_sync(0xffffffffu, __float_as_uint(a)), scale[i], by[i]);
+    }
+    if (lane == 0) {
+        s[0] = scale[0];
+        if (left > kQGroup) s[1] = scale[1];
+    }
+    Codes<false> c;
+    c.v = make_uint2(Q8<FMT>::encode4(mul2(f[0], both(by[0])), mul2(f[1], both(by[0]))),
+                     Q8<FMT>::encode4(mul2(f[2], both(by[1])), mul2(f[3], both(by[1]))));
+    c.store(q, lane, left);
+}
+
+// Quantises a warp's V adjacent segments of a row, the first starting at
+// column c0, into the row's codes q and scales s.
+template <int FMT, bool VEC, int V>
+__device__ __forceinline__ void quantise_row(const Lane8 (&f)[V], uint8_t* q, float* s, int c0,
+                                             int cols, int lane) {
+    if constexpr (VEC) {
+        uint32_t m[V];
+        float by[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) m[k] = own_amax(f[k]);
+        const float scale = group_scales<FMT, kF32, V>(m, lane, by);
+        const int g = c0 / kQGroup + 2 * group_carried<V>(lane) + (lane >> 4);
+        if (group_writer<V>(lane) && g * kQGroup < cols) s[g] = scale;
+#pragma unroll
+        for (int k = 0; k < V; ++k) encode8<FMT>(f[k], by[k], q + c0 + k * kSeg, lane, cols - c0 - k * kSeg);
     } else {
-        group_scale<FMT>(m[1], scale[1], by[1]);
-        if (lane == 0) {
-            s[0] = scale[0];
-            if (left > kQGroup) s[1] = scale[1];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = c0 + k * kSeg;
+            if (cols > c) quantise_any<FMT>(f[k], q + c, s + c / kQGroup, lane, cols - c);
         }
     }
-    float t[kEl];
-#pragma unroll
-    for (int j = 0; j < kEl; ++j) t[j] = __fmul_rn(f[j], by[j / 4]);
-    Codes<VEC> c;
-    c.v = make_uint2(Q8<FMT>::encode4(t[0], t[1], t[2], t[3]),
-                     Q8<FMT>::encode4(t[4], t[5], t[6], t[7]));
-    c.store(q, lane, left);
-}
-
-template <bool VEC>
-__device__ __forceinline__ void quantise8(int fmt, const float (&f)[kEl], const uint32_t (&m)[2],
-                                          uint8_t* q, float* s, int lane, int left) {
-    if (fmt == kE4M3) quantise8<kE4M3, VEC>(f, m, q, s, lane, left);
-    else quantise8<kInt8, VEC>(f, m, q, s, lane, left);
 }
 
 // ---------------------------------------------------------- sums over a row
 
 // The warps of one row: `n` of them, this one being `w`; `bar` their named
-// barrier, `red` 2 x n float2 of shared memory.  A sum's partials alternate
-// between the two halves of `red`, so one barrier a sum is enough: a half is
-// written again only after the next sum's barrier, which every warp passes
-// after reading it.
+// barrier, `red` 2 x 2 x 32 floats of shared memory, zero from n on.  A sum's
+// partials alternate between the two halves of `red`, so one barrier a sum is
+// enough: a half is written again only after the next sum's barrier, which
+// every warp passes after reading it.  The order of the additions is fixed.
+constexpr int kRowFloats = 128;
+template <int MOST>   // warps of a row at most
 struct RowWarps {
     int n, w, lane, bar;
-    float2* red;
+    float* red;
     int half;
-    __device__ __forceinline__ float2 sum(float a, float b) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        if (n == 1) return make_float2(a, b);
-        float2* r = red + half * n;
-        half ^= 1;
-        if (lane == 0) r[w] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n * 32) : "memory");
-        float2 t = lane < n ? r[lane] : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-            t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
-        }
-        return t;
+    // `all`: this block's kRowFloats floats for each of its rows.
+    __device__ __forceinline__ RowWarps(int row_warps, float* all) {
+        const int warp = threadIdx.x >> 5;
+        const int y = warp / row_warps;
+        n = row_warps;
+        w = warp - y * row_warps;
+        lane = threadIdx.x & 31;
+        bar = 1 + y;
+        red = all + y * kRowFloats;
+        half = 0;
+        if (w == 0)
+            for (int i = lane; i < kRowFloats; i += 32) red[i] = 0.f;
+        __syncthreads();
     }
-    __device__ __forceinline__ float sum(float a) { return sum(a, 0.f).x; }
+    template <int N>
+    __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (n == 1) return;
+        float* r = red + half * 64;
+        half ^= 1;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i * 32 + w] = v[i];
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n * 32) : "memory");
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float4* q = reinterpret_cast<const float4*>(r + i * 32);
+            float4 t = q[0];
+#pragma unroll
+            for (int k = 1; k * 4 < MOST; ++k) {
+                const float4 a = q[k];
+                t.x += a.x;
+                t.y += a.y;
+                t.z += a.z;
+                t.w += a.w;
+            }
+            v[i] = (t.x + t.y) + (t.z + t.w);
+        }
+    }
+    __device__ __forceinline__ float sum(float2 a) {
+        float v[1] = {a.x + a.y};
+        sum(v);
+        return v[0];
+    }
+    __device__ __forceinline__ float2 sum(float2 a, float2 b) {
+        float v[2] = {a.x + a.y, b.x + b.y};
+        sum(v);
+        return make_float2(v[0], v[1]);
+    }
 };
+
+// ------------------------------------------- a thread's own asynchronous ring
+// Rows ahead of the one being worked on are copied into shared memory by the
+// very thread that will read them (cp.async), so that a ring needs neither
+// barriers nor flags between threads: a thread waits for its own copies only.
+
+// (where `on`; the predicate in the instruction keeps branches out of the loops)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (BYTES == 16)
+        asm volatile("{ .reg .pred p; setp.ne.b32 p, %2, 0;\n\t"
+                     "@p cp.async.cg.shared.global [%0], [%1], 16; }" ::"r"(d), "l"(src), "r"((int)on)
+                     : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.ne.b32 p, %2, 0;\n\t"
+                     "@p cp.async.ca.shared.global [%0], [%1], %3; }" ::"r"(d), "l"(src),
+                     "r"((int)on), "n"(BYTES)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of the groups that copies_end() closed are still on the way.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Host: whether a pointer is on a 16-byte boundary (null is).
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
