@@ -206,6 +206,7 @@ __device__ __forceinline__ void load_param(const float* p, int64_t col0, int lan
 template <int FMT> struct Q8;
 template <> struct Q8<kE4M3> {
     static constexpr float kMax = 448.f;
+    static __device__ __forceinline__ float2 times(float2 v, float by) { return mul2(v, both(by)); }
     static __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
         const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
@@ -222,6 +223,11 @@ template <> struct Q8<kE4M3> {
 };
 template <> struct Q8<kInt8> {
     static constexpr float kMax = 127.f;
+    // One value at a time: mul2 and the addition below would be made one fused
+    // operation, which rounds once where the format says twice.
+    static __device__ __forceinline__ float2 times(float2 v, float by) {
+        return make_float2(__fmul_rn(v.x, by), __fmul_rn(v.y, by));
+    }
     // |v| <= 127: adding 1.5 * 2^23 leaves round-to-nearest-even(v) in the low
     // byte (two's complement).
     static __device__ __forceinline__ uint32_t encode4(float2 a, float2 b) {
@@ -391,8 +397,8 @@ __device__ __forceinline__ bool group_writer(int lane) {
 template <int FMT>
 __device__ __forceinline__ void encode8(const Lane8& f, float by, uint8_t* q, int lane, int left) {
     Codes<true> c;
-    c.v = make_uint2(Q8<FMT>::encode4(mul2(f[0], both(by)), mul2(f[1], both(by))),
-                     Q8<FMT>::encode4(mul2(f[2], both(by)), mul2(f[3], both(by))));
+    c.v = make_uint2(Q8<FMT>::encode4(Q8<FMT>::times(f[0], by), Q8<FMT>::times(f[1], by)),
+                     Q8<FMT>::encode4(Q8<FMT>::times(f[2], by), Q8<FMT>::times(f[3], by)));
     c.store(q, lane, left);
 }
 
@@ -413,8 +419,8 @@ __device__ __forceinline__ void quantise_any(const Lane8& f, uint8_t* q, float* 
         if (left > kQGroup) s[1] = scale[1];
     }
     Codes<false> c;
-    c.v = make_uint2(Q8<FMT>::encode4(mul2(f[0], both(by[0])), mul2(f[1], both(by[0]))),
-                     Q8<FMT>::encode4(mul2(f[2], both(by[1])), mul2(f[3], both(by[1]))));
+    c.v = make_uint2(Q8<FMT>::encode4(Q8<FMT>::times(f[0], by[0]), Q8<FMT>::times(f[1], by[0])),
+                     Q8<FMT>::encode4(Q8<FMT>::times(f[2], by[1]), Q8<FMT>::times(f[3], by[1])));
     c.store(q, lane, left);
 }
 
