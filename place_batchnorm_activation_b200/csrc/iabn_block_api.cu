@@ -202,7 +202,7 @@ iabn_status block_fwd_call(const iabn_block_desc* d, const void* u, const void* 
 size_t block_ws_bytes(const iabn_block_desc* d) {
     const int64_t workers = block_bwd_workers(d->rows, d->cols);
     const int64_t rows = 2 * block_bwd_slots(workers, gate_rows(d)) + 2 * workers;
-    return ((size_t)rows * (size_t)d->cols * sizeof(float) + 255) / 256 * 256;
+    return ((size_t)rows * (size_t)((d->cols + 3) / 4 * 4) * sizeof(float) + 255) / 256 * 256;
 }
 
 iabn_status block_bwd_call(const iabn_block_desc* d, bool codes, const void* su,

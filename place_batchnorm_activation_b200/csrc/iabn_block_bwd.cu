@@ -32,292 +32,668 @@ __host__ __device__ inline Span worker_rows(int64_t w, int64_t rows, int64_t wor
     return {w * rows / workers, (w + 1) * rows / workers};
 }
 
-template <int DT, bool VEC, int V, bool CODES, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_bwd_rows(const BlockBwd p, int row_warps) {
-    using T = typename Storage<DT>::T;
-    extern __shared__ float4 shared[];   // sums of a row, then (several rows a CTA) of columns
-    const int warp = threadIdx.x >> 5;
-    const int lanes_y = (blockDim.x >> 5) / row_warps;
-    RowWarps<32> rw(row_warps, reinterpret_cast<float*>(shared));
-    const int y = rw.bar - 1;
-    float* columns = reinterpret_cast<float*>(shared) + lanes_y * kRowFloats;
-    const float inv_n = 1.f / (float)p.cols;
-    const int64_t D = p.cols;
-    const int64_t slots = block_bwd_slots(p.workers, p.gates);
-    Lane8 A[V], B[V], C[V], E[V];
+// Columns as workspace rows hold them: whole 16-byte vectors.
+__host__ __device__ inline int64_t work_cols(int64_t cols) { return (cols + 3) / 4 * 4; }
+
+// Adds a block's rows (`rows` of them, this one being y) and writes one
+// partial-sum row; s starts again from zero.  The whole block calls it.
+template <bool VEC, int V, class RW>
+__device__ __forceinline__ void flush(Lane8 (&s)[V], float* out, int cols, int y, int rows,
+                                      const RW& rw, float* columns) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c0 = (rw.w * V + k) * kSeg, left = cols - c0;
+        if (rows > 1) {
+            __syncthreads();
+            float* mine = columns + (y * rw.n + rw.w) * kSeg;
+#pragma unroll
+            for (int j = 0; j < kEl; ++j) mine[rw.lane + 32 * j] = el(s[k], j);
+            __syncthreads();
+            if (y == 0)
+                for (int o = 1; o < rows; ++o) {
+                    const float* other = columns + (o * rw.n + rw.w) * kSeg;
+#pragma unroll
+                    for (int j = 0; j < kEl; ++j) el(s[k], j) += other[rw.lane + 32 * j];
+                }
+        }
+        if (y == 0) {
+            if (VEC) {
+                if (rw.lane * kEl < left) {
+                    float4* q = reinterpret_cast<float4*>(out + c0 + rw.lane * kEl);
+                    q[0] = make_float4(s[k][0].x, s[k][0].y, s[k][1].x, s[k][1].y);
+                    q[1] = make_float4(s[k][2].x, s[k][2].y, s[k][3].x, s[k][3].y);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kEl; ++j)
+                    if (rw.lane + 32 * j < left) out[c0 + rw.lane + 32 * j] = el(s[k], j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kEl / 2; ++j) s[k][j] = both(0.f);
+    }
+}
+
+// A worker's rows in steps of the block's row count, none of which crosses
+// from one gate row's tokens into the next's.
+struct Steps {
+    int64_t at, hi, end, per, gate;
+    int rows;
+    __device__ __forceinline__ Steps(const BlockBwd& p, int rows_cta) {
+        const Span s = worker_rows(blockIdx.x, p.rows, p.workers);
+        at = s.lo;
+        end = s.hi;
+        per = p.rows_per_gate;
+        rows = rows_cta;
+        open();
+    }
+    __device__ __forceinline__ void open() {   // the gate row that `at` is in
+        gate = per > 0 ? at / per : 0;
+        hi = per > 0 && (gate + 1) * per < end ? (gate + 1) * per : end;
+    }
+    __device__ __forceinline__ bool done() const { return at >= end; }
+    __device__ __forceinline__ bool last() const { return at + rows >= hi; }   // of this gate row
+    __device__ __forceinline__ void next() {
+        if (last()) {
+            at = hi;
+            open();
+        } else {
+            at += rows;
+        }
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void zero(Lane8 (&s)[V]) {
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
-        for (int j = 0; j < kEl / 2; ++j) A[k][j] = B[k][j] = C[k][j] = E[k][j] = both(0.f);
+        for (int j = 0; j < kEl / 2; ++j) s[k][j] = both(0.f);
+}
 
-    // Adds the CTA's row lanes and writes a partial-sum row.
-    auto flush = [&](Lane8 (&s)[V], float* out) {
+// Columns of a segment past the row's end are kept at zero where a LAYER
+// norm's mean would have moved them.
+template <bool VEC>
+__device__ __forceinline__ void mask8(Lane8& f, int lane, int left) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-            if (lanes_y > 1) {
-                __syncthreads();
-                float* mine = columns + warp * kSeg;
+    for (int j = 0; j < kEl; ++j)
+        if (seg_col<VEC>(lane, j) >= left) el(f, j) = 0.f;
+}
+
+// The kept tensor's values as normalised ones.
+__device__ __forceinline__ void kept_hat(Lane8& f, float mean, float rstd) {
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) mine[rw.lane + 32 * j] = el(s[k], j);
-                __syncthreads();
-                if (y == 0)
-                    for (int o = 1; o < lanes_y; ++o) {
-                        const float* other = columns + (o * rw.n + rw.w) * kSeg;
+    for (int j = 0; j < kEl / 2; ++j) f[j] = mul2(add2(f[j], both(-mean)), both(rstd));
+}
+
+// A row between its loads and its stores, shared by the kernels below.
+// First half: from g = dn and x = xhat, C += g x, E += g, g *= gamma_pre, and
+// the row's sums (level, slope) of g and g x.
+template <bool FULL, int V, class RW, class G>
+__device__ __forceinline__ float2 pre_half(Lane8 (&g)[V], const Lane8 (&x)[V], Lane8 (&C)[V],
+                                           Lane8 (&E)[V], RW& rw, const G& gamma) {
+    float2 s = both(0.f), sx = both(0.f);
 #pragma unroll
-                        for (int j = 0; j < kEl; ++j) el(s[k], j) += other[rw.lane + 32 * j];
-                    }
-            }
-            if (y == 0) {
+    for (int k = 0; k < V; ++k) {
+        Lane8 ga;
+        gamma(k, ga);
 #pragma unroll
-                for (int j = 0; j < kEl; ++j) {
-                    const int c = seg_col<VEC>(rw.lane, j);
-                    if (c < left) out[c0 + c] = el(s[k], j);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kEl / 2; ++j) s[k][j] = both(0.f);
+        for (int j = 0; j < kEl / 2; ++j) {
+            C[k][j] = fma2(g[k][j], x[k][j], C[k][j]);
+            if (FULL) E[k][j] = add2(E[k][j], g[k][j]);
+            g[k][j] = mul2(g[k][j], ga[j]);
+            if (FULL) s = add2(s, g[k][j]);
+            sx = fma2(g[k][j], x[k][j], sx);
         }
-    };
+    }
+    if (FULL) return rw.sum(s, sx);
+    return make_float2(0.f, rw.sum(sx));
+}
 
+// g becomes rstd (g - level - x slope).
+template <bool VEC, bool FULL, int V, class RW>
+__device__ __forceinline__ void back_through(Lane8 (&g)[V], const Lane8 (&x)[V], float level,
+                                             float slope, float rstd, int cols, const RW& rw) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int j = 0; j < kEl / 2; ++j) {
+            const float2 d = FULL ? add2(g[k][j], both(-level)) : g[k][j];
+            g[k][j] = mul2(fma2(x[k][j], both(-slope), d), both(rstd));
+        }
+        if (FULL) mask8<VEC>(g[k], rw.lane, cols - (rw.w * V + k) * kSeg);
+    }
+}
+
+// Second half: from t and x = uhat, A += t x, B += t, t *= gate gamma_post,
+// and the row's sums of t and t x.
+template <bool FULL, int V, class RW, class G>
+__device__ __forceinline__ float2 post_half(Lane8 (&t)[V], const Lane8 (&x)[V], Lane8 (&A)[V],
+                                            Lane8 (&B)[V], RW& rw, bool sums, const G& weight) {
+    float2 s = both(0.f), sx = both(0.f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        Lane8 ga;
+        weight(k, ga);
+#pragma unroll
+        for (int j = 0; j < kEl / 2; ++j) {
+            A[k][j] = fma2(t[k][j], x[k][j], A[k][j]);
+            if (FULL) B[k][j] = add2(B[k][j], t[k][j]);
+            t[k][j] = mul2(t[k][j], ga[j]);
+            if (FULL) s = add2(s, t[k][j]);
+            sx = fma2(t[k][j], x[k][j], sx);
+        }
+    }
+    if (!sums) return make_float2(0.f, 0.f);
+    if (FULL) return rw.sum(s, sx);
+    return make_float2(0.f, rw.sum(sx));
+}
+
+// gate gamma_post of a segment (either may be null: 1).
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const float* gamma, const float* gate, int c0, int lane,
+                                            int left, Lane8& f) {
+    load_param<VEC>(gamma, c0, lane, left, 1.f, f);
+    if (!gate) return;
+    Lane8 g;
+    load_param<VEC>(gate, c0, lane, left, 1.f, g);
+#pragma unroll
+    for (int j = 0; j < kEl / 2; ++j) f[j] = mul2(f[j], g[j]);
+}
+
+// The sums of a finished gate row, and of a finished worker.
+template <bool VEC, bool FULL, int V, class RW>
+__device__ __forceinline__ void flush_gate(const BlockBwd& p, int64_t gate, Lane8 (&A)[V],
+                                           Lane8 (&B)[V], int y, int rows, const RW& rw, float* columns) {
+    const int64_t W = work_cols(p.cols), slots = block_bwd_slots(p.workers, p.gates);
+    const int64_t slot = blockIdx.x + gate;
+    flush<VEC, V>(A, p.work + slot * W, p.cols, y, rows, rw, columns);
+    if (FULL) flush<VEC, V>(B, p.work + (slots + slot) * W, p.cols, y, rows, rw, columns);
+}
+template <bool VEC, bool FULL, int V, class RW>
+__device__ __forceinline__ void flush_worker(const BlockBwd& p, Lane8 (&C)[V], Lane8 (&E)[V], int y,
+                                             int rows, const RW& rw, float* columns) {
+    const int64_t W = work_cols(p.cols), slots = block_bwd_slots(p.workers, p.gates);
+    flush<VEC, V>(C, p.work + (2 * slots + blockIdx.x) * W, p.cols, y, rows, rw, columns);
+    if (FULL)
+        flush<VEC, V>(E, p.work + (2 * slots + p.workers + blockIdx.x) * W, p.cols, y, rows, rw, columns);
+}
+
+// Any width and alignment: each row is loaded as its turn comes.
+template <int DT, bool VEC, int V, int FMT>
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_bwd_any(const BlockBwd p, int row_warps) {
+    using T = typename Storage<DT>::T;
+    extern __shared__ float4 shared[];   // sums of a row, then (several rows a block) of columns
+    const int rows_cta = (blockDim.x >> 5) / row_warps;
+    RowWarps<V == 4 ? 32 : 16> rw(row_warps, reinterpret_cast<float*>(shared));
+    const int y = rw.bar - 1;
+    float* columns = reinterpret_cast<float*>(shared) + rows_cta * kRowFloats;
+    const float inv_n = 1.f / (float)p.cols;
+    const int64_t D = p.cols;
+    const int c0 = rw.w * V * kSeg;
+    Lane8 A[V], B[V], C[V], E[V];
+    zero(A);
+    zero(B);
+    zero(C);
+    zero(E);
     // The normalised segment k of a row: from codes, or from the kept tensor.
     auto hat = [&](const void* src, const float* scales, const float* means, const float* rstds,
                    int64_t row, int k, Lane8& f) {
-        const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-        if (CODES) {
-            Codes<VEC> c;
+        const int c = c0 + k * kSeg, left = p.cols - c;
+        if constexpr (FMT != kNoCodes) {
+            Codes<VEC> q;
             float sc[2] = {0.f, 0.f};
-            c.load(static_cast<const uint8_t*>(src) + row * D + c0, rw.lane, left);
-            load_scales<VEC>(scales + row * p.groups + c0 / kQGroup, rw.lane, left, sc);
-            if (p.format == kE4M3) c.template get<kE4M3>(sc, f);
-            else c.template get<kInt8>(sc, f);
+            q.load(static_cast<const uint8_t*>(src) + row * D + c, rw.lane, left);
+            load_scales<VEC>(scales + row * p.groups + c / kQGroup, rw.lane, left, sc);
+            q.template get<FMT>(sc, f);
         } else {
             Raw<DT, VEC> r;
-            r.load(static_cast<const T*>(src) + row * D + c0, rw.lane, left);
+            r.load(static_cast<const T*>(src) + row * D + c, rw.lane, left);
             r.get(f);
-            const float mean = means ? __ldg(means + row) : 0.f;
-            const float rstd = rstds ? __ldg(rstds + row) : 1.f;
-#pragma unroll
-            for (int j = 0; j < kEl; ++j)
-                el(f, j) = seg_col<VEC>(rw.lane, j) < left ? (el(f, j) - mean) * rstd : 0.f;
+            kept_hat(f, means ? __ldg(means + row) : 0.f, rstds ? __ldg(rstds + row) : 1.f);
+            mask8<VEC>(f, rw.lane, left);
         }
     };
-
-    const Span mine = worker_rows(blockIdx.x, p.rows, p.workers);
-    for (int64_t lo = mine.lo; lo < mine.hi;) {
-        const int64_t gr = p.rows_per_gate > 0 ? lo / p.rows_per_gate : 0;
-        const int64_t end = p.rows_per_gate > 0 ? (gr + 1) * p.rows_per_gate : mine.hi;
-        const int64_t hi = end < mine.hi ? end : mine.hi;
-        const float* gate = p.gate ? p.gate + gr * D : nullptr;
-        for (int64_t row = lo + y; row < hi; row += lanes_y) {
-            Lane8 t[V];
+    for (Steps st(p, rows_cta); !st.done(); st.next()) {
+        const int64_t row = st.at + y;
+        if (row < st.hi) {
+            Lane8 t[V], x[V];
+            zero(t);
             if (p.dh_out) {
                 Raw<DT, VEC> r[V];
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int c0 = (k * rw.n + rw.w) * kSeg;
-                    r[k].load(static_cast<const T*>(p.dh_out) + row * D + c0, rw.lane, p.cols - c0);
-                }
+                for (int k = 0; k < V; ++k)
+                    r[k].load(static_cast<const T*>(p.dh_out) + row * D + c0 + k * kSeg, rw.lane,
+                              p.cols - c0 - k * kSeg);
 #pragma unroll
                 for (int k = 0; k < V; ++k) r[k].get(t[k]);
-            } else {
+            }
+            if (p.pre != kNormNone) {
+                Lane8 g[V];
+                Raw<DT, VEC> r[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    r[k].load(static_cast<const T*>(p.dn) + row * D + c0 + k * kSeg, rw.lane,
+                              p.cols - c0 - k * kSeg);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    hat(p.sh, p.scale_pre, p.mean_pre, p.rstd_pre, row, k, x[k]);
+                    r[k].get(g[k]);
+                }
+                const float2 m = pre_half<true, V>(g, x, C, E, rw, [&](int k, Lane8& f) {
+                    load_param<VEC>(p.gamma_pre, c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, 1.f, f);
+                });
+                back_through<VEC, true, V>(g, x, p.pre == kNormLayer ? m.x * inv_n : 0.f, m.y * inv_n,
+                                           __ldg(p.rstd_pre + row), p.cols, rw);
 #pragma unroll
                 for (int k = 0; k < V; ++k)
 #pragma unroll
-                    for (int j = 0; j < kEl / 2; ++j) t[k][j] = both(0.f);
+                    for (int j = 0; j < kEl / 2; ++j) t[k][j] = add2(t[k][j], g[k][j]);
             }
-            if (p.pre != kNormNone) {
-                Lane8 g[V], x[V];
-                float2 s = both(0.f), sx = both(0.f);
+            zero(x);
+            if (p.su)
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-                    Raw<DT, VEC> r;
-                    r.load(static_cast<const T*>(p.dn) + row * D + c0, rw.lane, left);
-                    hat(p.sh, p.scale_pre, p.mean_pre, p.rstd_pre, row, k, x[k]);
-                    r.get(g[k]);
-                    Lane8 ga;
-                    load_param<VEC>(p.gamma_pre, c0, rw.lane, left, 1.f, ga);
-#pragma unroll
-                    for (int j = 0; j < kEl / 2; ++j) {
-                        C[k][j] = fma2(g[k][j], x[k][j], C[k][j]);
-                        E[k][j] = add2(E[k][j], g[k][j]);
-                        g[k][j] = mul2(g[k][j], ga[j]);
-                        s = add2(s, g[k][j]);
-                        sx = fma2(g[k][j], x[k][j], sx);
-                    }
-                }
-                const float2 m = rw.sum(s, sx);
-                const float level = p.pre == kNormLayer ? m.x * inv_n : 0.f, slope = m.y * inv_n;
-                const float rstd = __ldg(p.rstd_pre + row);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int left = p.cols - (k * rw.n + rw.w) * kSeg;
-#pragma unroll
-                    for (int j = 0; j < kEl; ++j) {
-                        const float d = fmaf(-slope, el(x[k], j), el(g[k], j) - level);
-                        if (seg_col<VEC>(rw.lane, j) < left) el(t[k], j) = fmaf(rstd, d, el(t[k], j));
-                    }
-                }
-            }
-            Lane8 x[V];
-            float2 s = both(0.f), sx = both(0.f);
+                for (int k = 0; k < V; ++k)
+                    hat(p.su, p.scale_post, p.mean_post, p.rstd_post, row, k, x[k]);
+            // (all inputs of these columns have been read: dh may be any of them)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const int c0 = (k * rw.n + rw.w) * kSeg, left = p.cols - c0;
-                if (p.su) {
-                    hat(p.su, p.scale_post, p.mean_post, p.rstd_post, row, k, x[k]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kEl / 2; ++j) x[k][j] = both(0.f);
-                }
-                // (all inputs of this column have been read: dh may be any of them)
                 Lane8 o;
 #pragma unroll
                 for (int j = 0; j < kEl / 2; ++j) o[j] = mul2(both(p.alpha), t[k][j]);
-                store8<DT, VEC>(static_cast<T*>(p.dh) + row * D + c0, rw.lane, left, o);
-                Lane8 ga, gt;
-                load_param<VEC>(p.gamma_post, c0, rw.lane, left, 1.f, ga);
-                load_param<VEC>(gate, c0, rw.lane, left, 1.f, gt);
-#pragma unroll
-                for (int j = 0; j < kEl / 2; ++j) {
-                    A[k][j] = fma2(t[k][j], x[k][j], A[k][j]);
-                    B[k][j] = add2(B[k][j], t[k][j]);
-                    t[k][j] = mul2(t[k][j], mul2(gt[j], ga[j]));
-                    s = add2(s, t[k][j]);
-                    sx = fma2(t[k][j], x[k][j], sx);
-                }
+                store8<DT, VEC>(static_cast<T*>(p.dh) + row * D + c0 + k * kSeg, rw.lane,
+                                p.cols - c0 - k * kSeg, o);
             }
-            if (!p.du) continue;
-            if (p.post != kNormNone) {
-                const float2 m = rw.sum(s, sx);
-                const float level = p.post == kNormLayer ? m.x * inv_n : 0.f, slope = m.y * inv_n;
-                const float rstd = __ldg(p.rstd_post + row);
+            const float* gate = p.gate ? p.gate + st.gate * D : nullptr;
+            const float2 m = post_half<true, V>(t, x, A, B, rw, p.post != kNormNone, [&](int k, Lane8& f) {
+                load_weight<VEC>(p.gamma_post, gate, c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, f);
+            });
+            if (p.post != kNormNone)
+                back_through<VEC, true, V>(t, x, p.post == kNormLayer ? m.x * inv_n : 0.f, m.y * inv_n,
+                                           __ldg(p.rstd_post + row), p.cols, rw);
+            if (p.du)
 #pragma unroll
                 for (int k = 0; k < V; ++k)
+                    store8<DT, VEC>(static_cast<T*>(p.du) + row * D + c0 + k * kSeg, rw.lane,
+                                    p.cols - c0 - k * kSeg, t[k]);
+        }
+        if (st.last()) flush_gate<VEC, true, V>(p, st.gate, A, B, y, rows_cta, rw, columns);
+    }
+    flush_worker<VEC, true, V>(p, C, E, y, rows_cta, rw, columns);
+}
+
+// VEC widths up to 8192: a thread copies its share of the rows to come into a
+// ring of its own, two rows ahead, dn and xhat in one group of copies, dh' and
+// uhat in the next: each half of a slot is filled again as soon as the thread
+// has read it.
+constexpr int kBwdV = 2;          // segments a warp
+constexpr int kBwdThreads = 256;  // a block's least threads (several rows, if need be)
+
+// Shared memory of a thread, in 16-byte quads: gate*gamma_post and gamma_pre,
+// and two slots of dn, dh', xhat and uhat.
+template <int DT, int V, int FMT>
+struct BwdShared {
+    static constexpr int Q = Raw<DT, true>::kQuads;
+    static constexpr int kCoef = 2 * V * 2;
+    static constexpr int kHalf = FMT == kNoCodes ? 2 * V * Q : V * Q + (V + 1) / 2;   // dn, xhat | dh', uhat
+    static constexpr int kQuads = kCoef + 4 * kHalf;
+};
+
+template <int DT, int V, int FMT, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) block_bwd(const BlockBwd p, int row_warps) {
+    using T = typename Storage<DT>::T;
+    using S = BwdShared<DT, V, FMT>;
+    constexpr int Q = S::Q;
+    constexpr bool CODES = FMT != kNoCodes;
+    extern __shared__ float4 shared[];
+    __shared__ __align__(16) float red[8 * kRowFloats];
+    const int rows_cta = (blockDim.x >> 5) / row_warps;
+    RowWarps<MAXT / 32> rw(row_warps, red);
+    const int y = rw.bar - 1;
+    float4* mine = shared + threadIdx.x;   // quad i of the thread: mine[i * blockDim.x]
+    const float inv_n = 1.f / (float)p.cols;
+    const int c0 = rw.w * V * kSeg;
+    const int col = c0 + rw.lane * kEl;
+    const int sgrp = (c0 >> 7) + (rw.lane >> 4);   // the lane's scale, of segment 0
+    const bool has_pre = p.pre != kNormNone;
+
+    // half 0: dn and xhat, half 1: dh' and uhat; quads of slot `slot`
+    auto quad = [&](int slot, int half, int i) {
+        return mine + (S::kCoef + (slot * 2 + half) * S::kHalf + i) * blockDim.x;
+    };
+    // where codes lie: segment k's 8 bytes in a 16-byte quad
+    auto code = [&](int slot, int half, int k) {
+        return reinterpret_cast<uint2*>(quad(slot, half, V * Q + k / 2)) + (k & 1);
+    };
+    auto fetch = [&](int slot, int half, int64_t row, bool on) {
+        const T* a = static_cast<const T*>(half == 0 ? p.dn : p.dh_out);
+        const void* b = half == 0 ? p.sh : p.su;
+        const int64_t at = row * p.cols + col;
 #pragma unroll
-                    for (int j = 0; j < kEl; ++j)
-                        el(t[k], j) = rstd * fmaf(-slope, el(x[k], j), el(t[k], j) - level);
+        for (int k = 0; k < V; ++k) {
+            const bool in = on && col + k * kSeg < p.cols;
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                copy_async<16>(quad(slot, half, k * Q + i), a + at + k * kSeg + i * 4, in && a);
+            if constexpr (CODES) {
+                copy_async<8>(code(slot, half, k), static_cast<const uint8_t*>(b) + at + k * kSeg, in && b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+                    copy_async<16>(quad(slot, half, (V + k) * Q + i),
+                                   static_cast<const T*>(b) + at + k * kSeg + i * 4, in && b);
             }
+        }
+        copies_end();
+    };
+    // what no copy writes (past the row's end, a tensor that is not there) reads as zero
+    for (int i = 0; i < S::kQuads; ++i) mine[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    // a row's statistics and scales, read a row ahead
+    struct Row {
+        float rstd_pre, rstd_post, mean_pre, mean_post;
+        float scale_pre[V], scale_post[V];
+    };
+    auto row_of = [&](Row& r, int64_t row, bool on) {
+        r.rstd_pre = on && p.rstd_pre ? __ldg(p.rstd_pre + row) : 1.f;
+        r.rstd_post = on && p.rstd_post ? __ldg(p.rstd_post + row) : 1.f;
+        if constexpr (CODES) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const int c0 = (k * rw.n + rw.w) * kSeg;
-                store8<DT, VEC>(static_cast<T*>(p.du) + row * D + c0, rw.lane, p.cols - c0, t[k]);
+                const bool in = on && col + k * kSeg < p.cols;
+                const int64_t at = row * p.groups + sgrp + 2 * k;
+                r.scale_pre[k] = in && p.sh ? __ldg(p.scale_pre + at) : 0.f;
+                r.scale_post[k] = in && p.su ? __ldg(p.scale_post + at) : 0.f;
             }
+        } else if constexpr (FULL) {
+            r.mean_pre = on && p.mean_pre ? __ldg(p.mean_pre + row) : 0.f;
+            r.mean_post = on && p.mean_post ? __ldg(p.mean_post + row) : 0.f;
         }
-        const int64_t slot = blockIdx.x + gr;
-        flush(A, p.work + slot * D);
-        flush(B, p.work + (slots + slot) * D);
-        lo = hi;
+    };
+    auto hat = [&](int slot, int half, int k, const Row& r, Lane8& f) {
+        if constexpr (CODES) {
+            Codes<true> c;
+            c.v = *code(slot, half, k);
+            const float s = half == 0 ? r.scale_pre[k] : r.scale_post[k];
+            const float two[2] = {s, s};
+            c.template get<FMT>(two, f);
+        } else {
+            Raw<DT, true> q;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, (V + k) * Q + i));
+            q.get(f);
+            kept_hat(f, !FULL ? 0.f : half == 0 ? r.mean_pre : r.mean_post,
+                     half == 0 ? r.rstd_pre : r.rstd_post);
+            if (FULL) mask8<true>(f, rw.lane, p.cols - c0 - k * kSeg);
+        }
+    };
+    auto grad = [&](int slot, int half, int k, Lane8& f) {
+        Raw<DT, true> q;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, k * Q + i));
+        q.get(f);
+    };
+    auto coef = [&](int which, int k, Lane8& f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = mine[((which * V + k) * 2 + i) * blockDim.x];
+            f[2 * i] = make_float2(v.x, v.y);
+            f[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    };
+    auto set_coef = [&](int which, const float* gamma, const float* gate) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            Lane8 f;
+            load_weight<true>(gamma, gate, c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                mine[((which * V + k) * 2 + i) * blockDim.x] =
+                    make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+        }
+    };
+
+    Steps st(p, rows_cta), ahead(p, rows_cta);
+    auto fetch_next = [&](int slot, int half) { fetch(slot, half, ahead.at + y, !ahead.done() && ahead.at + y < ahead.hi); };
+    fetch_next(0, 0);
+    fetch_next(0, 1);
+    Row r;
+    row_of(r, st.at + y, st.at + y < st.hi);
+    ahead.next();
+    fetch_next(1, 0);
+    fetch_next(1, 1);
+    set_coef(1, p.gamma_pre, nullptr);
+    set_coef(0, p.gamma_post, p.gate ? p.gate + st.gate * p.cols : nullptr);
+    Lane8 A[V], B[V], C[V], E[V];
+    zero(A);
+    zero(C);
+    if (FULL) {
+        zero(B);
+        zero(E);
     }
-    flush(C, p.work + (2 * slots + blockIdx.x) * D);
-    flush(E, p.work + (2 * slots + p.workers + blockIdx.x) * D);
-}
-
-// The column pass: a block takes 32 columns, its 32 warps share the partial
-// sums of them.  blockIdx.y 0: dgamma_pre, dbeta_pre; 1: dgamma_post,
-// dbeta_post; from 2: the gate rows.
-constexpr int kColWarps = 32;
-
-__device__ __forceinline__ float add_warps(float v, float (&sh)[kColWarps][33]) {
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    __syncthreads();
-    sh[w][l] = v;
-    __syncthreads();
-    const float t = sh[l][w];   // column w of the block, partial l
-    return warp_sum(t);         // valid for column w
-}
-
-__global__ void __launch_bounds__(1024) block_bwd_columns(const BlockBwd p) {
-    __shared__ float sh[kColWarps][33];
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    const int64_t D = p.cols;
-    const int64_t c = (int64_t)blockIdx.x * 32 + l;       // column this thread reads
-    const int64_t co = (int64_t)blockIdx.x * 32 + w;      // column this warp writes
-    const bool in = c < D, out = co < D && l == 0;
-    const int64_t slots = block_bwd_slots(p.workers, p.gates);
-    const float* A = p.work;
-    const float* B = p.work + slots * D;
-    const float* C = p.work + 2 * slots * D;
-    const float* E = p.work + (2 * slots + p.workers) * D;
-    const int64_t P = p.rows > 0 ? p.workers : 0;
-    if (blockIdx.y == 0) {
-        float a = 0.f, b = 0.f;
-        for (int64_t i = w; i < P && in; i += kColWarps) {
-            a += C[i * D + c];
-            b += E[i * D + c];
+    for (int slot = 0; !st.done(); slot ^= 1) {
+        const int64_t row = st.at + y;
+        const bool here = row < st.hi;
+        Row now = r;   // and the next row's, whose step `ahead` is at
+        row_of(r, ahead.at + y, !ahead.done() && ahead.at + y < ahead.hi);
+        ahead.next();
+        copies_wait<3>();
+        Lane8 g[V], x[V], t[V];
+        if (has_pre)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                grad(slot, 0, k, g[k]);
+                hat(slot, 0, k, now, x[k]);
+            }
+        fetch_next(slot, 0);
+        if (here && has_pre) {
+            const float2 m = pre_half<FULL, V>(g, x, C, E, rw, [&](int k, Lane8& f) { coef(1, k, f); });
+            back_through<true, FULL, V>(g, x, FULL && p.pre == kNormLayer ? m.x * inv_n : 0.f, m.y * inv_n,
+                                        now.rstd_pre, p.cols, rw);
         }
-        a = add_warps(a, sh);
-        b = add_warps(b, sh);
-        if (out && p.dgamma_pre) p.dgamma_pre[co] = a;
-        if (out && p.dbeta_pre) p.dbeta_pre[co] = b;
+        copies_wait<3>();
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            grad(slot, 1, k, t[k]);
+            hat(slot, 1, k, now, x[k]);
+            if (has_pre)
+#pragma unroll
+                for (int j = 0; j < kEl / 2; ++j) t[k][j] = add2(t[k][j], g[k][j]);
+        }
+        fetch_next(slot, 1);
+        if (here) {
+            const int64_t at = row * p.cols + c0;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                Lane8 o;
+#pragma unroll
+                for (int j = 0; j < kEl / 2; ++j) o[j] = mul2(both(p.alpha), t[k][j]);
+                store8<DT, true>(static_cast<T*>(p.dh) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, o);
+            }
+            const float2 m = post_half<FULL, V>(t, x, A, B, rw, p.post != kNormNone,
+                                                [&](int k, Lane8& f) { coef(0, k, f); });
+            if (p.post != kNormNone)
+                back_through<true, FULL, V>(t, x, FULL && p.post == kNormLayer ? m.x * inv_n : 0.f,
+                                            m.y * inv_n, now.rstd_post, p.cols, rw);
+            if (p.du)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    store8<DT, true>(static_cast<T*>(p.du) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, t[k]);
+        }
+        const bool last = st.last();
+        if (last)   // (behind the ring and the coefficients: the rows' sums of columns)
+            flush_gate<true, FULL, V>(p, st.gate, A, B, y, rows_cta, rw,
+                                      reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+        st.next();
+        if (last && p.gate && p.rows_per_gate > 0 && !st.done())
+            set_coef(0, p.gamma_post, p.gate + st.gate * p.cols);
+    }
+    copies_wait<0>();
+    flush_worker<true, FULL, V>(p, C, E, y, rows_cta, rw, reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+}
+
+// The column pass: a block takes 128 columns, four a thread of a warp, its 16
+// warps share the partial sums of them.  blockIdx.y 0: dgamma_pre, dbeta_pre;
+// 1: dgamma_post, dbeta_post; from 2: the gate rows.
+constexpr int kColWarps = 16;
+
+__device__ __forceinline__ void add4(float4& a, float4 b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+__device__ __forceinline__ void fma4(float4& a, float4 w, float4 b) {
+    a.x = fmaf(w.x, b.x, a.x);
+    a.y = fmaf(w.y, b.y, a.y);
+    a.z = fmaf(w.z, b.z, a.z);
+    a.w = fmaf(w.w, b.w, a.w);
+}
+
+// The block's total of v, of column `threadIdx.x` (threads below 128).
+__device__ __forceinline__ float add_warps(float4 v, float4 (&sh)[kColWarps][32]) {
+    __syncthreads();
+    sh[threadIdx.x >> 5][threadIdx.x & 31] = v;
+    __syncthreads();
+    float t = 0.f;
+    if (threadIdx.x < 128)
+#pragma unroll
+        for (int w = 0; w < kColWarps; ++w) t += reinterpret_cast<const float*>(sh[w])[threadIdx.x];
+    return t;
+}
+
+__global__ void __launch_bounds__(32 * kColWarps) block_bwd_columns(const BlockBwd p) {
+    __shared__ float4 sh[kColWarps][32];
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    const int64_t W = work_cols(p.cols);
+    const int64_t c = (int64_t)blockIdx.x * 128 + 4 * l;          // columns this thread reads
+    const int64_t co = (int64_t)blockIdx.x * 128 + threadIdx.x;   // column it writes
+    const bool in = c < W, out = co < p.cols && threadIdx.x < 128;
+    const int64_t slots = block_bwd_slots(p.workers, p.gates);
+    const float* A = p.work + c;
+    const float* B = A + slots * W;
+    const float* C = B + slots * W;
+    const float* E = C + p.workers * W;
+    const int64_t P = p.rows > 0 ? p.workers : 0;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 a = none, b = none;
+    auto row = [&](const float* base, int64_t i) { return __ldcs(reinterpret_cast<const float4*>(base + i * W)); };
+    if (blockIdx.y == 0) {
+        if (in) {
+            if (p.dgamma_pre)
+#pragma unroll 4
+                for (int64_t i = w; i < P; i += kColWarps) add4(a, row(C, i));
+            if (p.dbeta_pre)
+#pragma unroll 4
+                for (int64_t i = w; i < P; i += kColWarps) add4(b, row(E, i));
+        }
+        const float ta = add_warps(a, sh), tb = add_warps(b, sh);
+        if (out && p.dgamma_pre) p.dgamma_pre[co] = ta;
+        if (out && p.dbeta_pre) p.dbeta_pre[co] = tb;
     } else if (blockIdx.y == 1) {
-        float a = 0.f, b = 0.f;
         for (int64_t i = w; i < P && in; i += kColWarps) {
             const Span r = worker_rows(i, p.rows, p.workers);
             const int64_t g0 = p.rows_per_gate > 0 ? r.lo / p.rows_per_gate : 0;
             const int64_t g1 = p.rows_per_gate > 0 ? (r.hi - 1) / p.rows_per_gate : 0;
             for (int64_t g = g0; g <= g1; ++g) {
-                const float gt = p.gate ? p.gate[g * D + c] : 1.f;
-                a = fmaf(gt, A[(i + g) * D + c], a);
-                b = fmaf(gt, B[(i + g) * D + c], b);
+                float4 gt = make_float4(1.f, 1.f, 1.f, 1.f);
+                if (p.gate) {
+                    const float* q = p.gate + g * p.cols + c;
+                    gt.x = __ldg(q);
+                    gt.y = c + 1 < p.cols ? __ldg(q + 1) : 0.f;
+                    gt.z = c + 2 < p.cols ? __ldg(q + 2) : 0.f;
+                    gt.w = c + 3 < p.cols ? __ldg(q + 3) : 0.f;
+                }
+                if (p.dgamma_post) fma4(a, gt, row(A, i + g));
+                if (p.dbeta_post) fma4(b, gt, row(B, i + g));
             }
         }
-        a = add_warps(a, sh);
-        b = add_warps(b, sh);
-        if (out && p.dgamma_post) p.dgamma_post[co] = a;
-        if (out && p.dbeta_post) p.dbeta_post[co] = b;
+        const float ta = add_warps(a, sh), tb = add_warps(b, sh);
+        if (out && p.dgamma_post) p.dgamma_post[co] = ta;
+        if (out && p.dbeta_post) p.dbeta_post[co] = tb;
     } else {
         for (int64_t g = blockIdx.y - 2; g < p.gates; g += gridDim.y - 2) {
-            float a = 0.f, b = 0.f;
-            if (P > 0) {
+            a = b = none;
+            if (P > 0 && in) {
                 const int64_t lo = p.rows_per_gate > 0 ? g * p.rows_per_gate : 0;
                 int64_t hi = p.rows_per_gate > 0 ? lo + p.rows_per_gate : p.rows;
                 if (hi > p.rows) hi = p.rows;
-                // workers whose ranges meet [lo, hi)
+                // the workers that hold rows lo and hi - 1
                 int64_t w0 = lo * P / p.rows, w1 = (hi - 1) * P / p.rows;
-                while (w0 > 0 && worker_rows(w0 - 1, p.rows, P).hi > lo) --w0;
                 while (worker_rows(w0, p.rows, P).hi <= lo) ++w0;
                 while (worker_rows(w1, p.rows, P).hi < hi) ++w1;
-                while (worker_rows(w1, p.rows, P).lo >= hi) --w1;
-                for (int64_t i = w0 + w; i <= w1 && in; i += kColWarps) {
-                    a += A[(i + g) * D + c];
-                    b += B[(i + g) * D + c];
+                for (int64_t i = w0 + w; i <= w1; i += kColWarps) {
+                    add4(a, row(A, i + g));
+                    if (p.beta_post) add4(b, row(B, i + g));
                 }
             }
-            a = add_warps(a, sh);
-            b = add_warps(b, sh);
+            const float ta = add_warps(a, sh), tb = add_warps(b, sh);
             if (out) {
                 const float ga = p.gamma_post ? p.gamma_post[co] : 1.f;
                 const float be = p.beta_post ? p.beta_post[co] : 0.f;
-                p.dgate[g * D + co] = fmaf(ga, a, be * b);
+                p.dgate[g * p.cols + co] = fmaf(ga, ta, be * tb);
             }
         }
     }
 }
 
-template <int DT, bool VEC, bool CODES, int V, int MAXT>
-cudaError_t launch(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
+template <int DT, bool VEC, int FMT, int V>
+cudaError_t launch_any(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
     const int threads = 32 * row_warps * rows_cta;
     const size_t smem = (rows_cta * kRowFloats + (rows_cta > 1 ? threads / 32 * kSeg : 0)) * sizeof(float);
-    block_bwd_rows<DT, VEC, V, CODES, MAXT><<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
+    block_bwd_any<DT, VEC, V, FMT><<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
     count_launches(1);
     return cudaGetLastError();
 }
 
-template <int DT, bool VEC, bool CODES>
-cudaError_t by_width(const BlockBwd& a, cudaStream_t s) {
+constexpr size_t kMostShared = 227 * 1024 - 8 * kRowFloats * sizeof(float);
+
+template <int DT, int FMT>
+size_t shared_bytes(int threads, int rows_cta) {
+    return (size_t)BwdShared<DT, kBwdV, FMT>::kQuads * 16 * threads +
+           (rows_cta > 1 ? threads / 32 * kSeg * sizeof(float) : 0);
+}
+
+template <int DT, int FMT, bool FULL>
+cudaError_t launch(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
+    const int threads = 32 * row_warps * rows_cta;
+    const size_t smem = shared_bytes<DT, FMT>(threads, rows_cta);
+    auto kernel = threads <= 256 ? block_bwd<DT, kBwdV, FMT, FULL, 256> : block_bwd<DT, kBwdV, FMT, FULL, 512>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int DT, int FMT>
+cudaError_t by_width(const BlockBwd& a, bool vec, cudaStream_t s) {
     const int segs = (a.cols + kSeg - 1) / kSeg;
-    if (segs <= 16)
-        return launch<DT, VEC, CODES, 1, 512>(a, segs, segs >= 8 ? 1 : 8 / segs, s);
-    if (segs <= 32) return launch<DT, VEC, CODES, 2, 512>(a, (segs + 1) / 2, 1, s);
-    return launch<DT, VEC, CODES, 4, 1024>(a, (segs + 3) / 4, 1, s);
+    if (vec && segs <= 32) {
+        const int row_warps = (segs + kBwdV - 1) / kBwdV;
+        const int rows_cta = row_warps * 32 >= kBwdThreads ? 1 : kBwdThreads / 32 / row_warps;
+        if (shared_bytes<DT, FMT>(32 * row_warps * rows_cta, rows_cta) <= kMostShared) {
+            const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.dbeta_post || a.dbeta_pre ||
+                              (a.dgate && a.beta_post);
+            return full ? launch<DT, FMT, true>(a, row_warps, rows_cta, s)
+                        : launch<DT, FMT, false>(a, row_warps, rows_cta, s);
+        }
+    }
+    if (segs <= 16) {
+        const int rows_cta = segs >= 8 ? 1 : 8 / segs;
+        return vec ? launch_any<DT, true, FMT, 1>(a, segs, rows_cta, s)
+                   : launch_any<DT, false, FMT, 1>(a, segs, rows_cta, s);
+    }
+    if (segs <= 32) return vec ? launch_any<DT, true, FMT, 2>(a, (segs + 1) / 2, 1, s)
+                               : launch_any<DT, false, FMT, 2>(a, (segs + 1) / 2, 1, s);
+    return vec ? launch_any<DT, true, FMT, 4>(a, (segs + 3) / 4, 1, s)
+               : launch_any<DT, false, FMT, 4>(a, (segs + 3) / 4, 1, s);
 }
 
 template <int DT>
-cudaError_t by_kind(const BlockBwd& a, bool vec, bool codes, cudaStream_t s) {
-    if (codes) return vec ? by_width<DT, true, true>(a, s) : by_width<DT, false, true>(a, s);
-    return vec ? by_width<DT, true, false>(a, s) : by_width<DT, false, false>(a, s);
+cudaError_t by_format(const BlockBwd& a, bool vec, bool codes, cudaStream_t s) {
+    if (!codes) return by_width<DT, kNoCodes>(a, vec, s);
+    return a.format == kE4M3 ? by_width<DT, kE4M3>(a, vec, s) : by_width<DT, kInt8>(a, vec, s);
 }
 
 }  // namespace
@@ -330,16 +706,16 @@ cudaError_t block_backward(const BlockBwd& a, int dtype, bool codes, cudaStream_
     if (a.rows > 0) {
         const bool vec = a.cols % kEl == 0 && on16(a.su) && on16(a.sh) && on16(a.dh_out) &&
                          on16(a.dn) && on16(a.dh) && on16(a.du);
-        const cudaError_t e = dtype == kF32    ? by_kind<kF32>(a, vec, codes, s)
-                              : dtype == kBF16 ? by_kind<kBF16>(a, vec, codes, s)
-                                               : by_kind<kF16>(a, vec, codes, s);
+        const cudaError_t e = dtype == kF32    ? by_format<kF32>(a, vec, codes, s)
+                              : dtype == kBF16 ? by_format<kBF16>(a, vec, codes, s)
+                                               : by_format<kF16>(a, vec, codes, s);
         if (e != cudaSuccess) return e;
     }
     const bool pre = a.dgamma_pre || a.dbeta_pre, post = a.dgamma_post || a.dbeta_post;
     if (!pre && !post && !a.dgate) return cudaSuccess;
     const int64_t gates = a.dgate ? (a.gates < 4096 ? a.gates : 4096) : 0;
-    const dim3 grid((unsigned)((a.cols + 31) / 32), (unsigned)(2 + gates));
-    block_bwd_columns<<<grid, 1024, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)(2 + gates));
+    block_bwd_columns<<<grid, 32 * kColWarps, 0, s>>>(a);
     count_launches(1);
     return cudaGetLastError();
 }

@@ -174,7 +174,7 @@ __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool h
 
 // Any width and alignment: each row is loaded as its turn comes.
 template <int DT, bool VEC, int V, int FMT>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) block_fwd_any(const BlockFwd p, int row_warps) {
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_fwd_any(const BlockFwd p, int row_warps) {
     using T = typename Storage<DT>::T;
     __shared__ __align__(16) float red[8 * kRowFloats];
     RowWarps<V == 4 ? 32 : 16> rw(row_warps, red);
