@@ -281,8 +281,8 @@ iabn_status block_bwd_call(const iabn_block_desc* d, bool codes, const void* su,
     a.dbeta_pre = dbeta_pre;
     a.work = static_cast<float*>(workspace);
     a.rows = d->rows;
-    a.rows_per_gate = d->rows_per_gate;
-    a.gates = gate_rows(d);
+    a.rows_per_gate = gate ? d->rows_per_gate : 0;
+    a.gates = gate ? gate_rows(d) : 1;
     a.workers = block_bwd_workers(d->rows, d->cols);
     a.cols = (int)d->cols;
     a.groups = (int)q_groups(d->cols);

@@ -23,14 +23,22 @@ void count_launches(int n);
 
 namespace {
 
-constexpr int kBwdCtas = 296;   // workers of the row pass at most
+// Workers of the row pass at most: one wave of its blocks on 148 SMs, two a
+// SM up to 4096 columns (256 threads each), one above.
+inline int64_t most_workers(int64_t cols) { return cols <= 4096 ? 296 : 148; }
 
-struct Span {
-    int64_t lo, hi;
+// Worker w's rows: rows / workers of them, one more for the first rows %
+// workers.  (32 bits: there are fewer than 2^31 rows.)
+struct Split {
+    int each, more;
+    __device__ __forceinline__ Split(const BlockBwd& p)
+        : each((int)p.rows / (int)p.workers), more((int)p.rows % (int)p.workers) {}
+    __device__ __forceinline__ int first(int w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int worker(int row) const {   // that holds the row
+        const int big = more * (each + 1);
+        return row < big ? row / (each + 1) : more + (row - big) / each;
+    }
 };
-__host__ __device__ inline Span worker_rows(int64_t w, int64_t rows, int64_t workers) {
-    return {w * rows / workers, (w + 1) * rows / workers};
-}
 
 // Columns as workspace rows hold them: whole 16-byte vectors.
 __host__ __device__ inline int64_t work_cols(int64_t cols) { return (cols + 3) / 4 * 4; }
@@ -77,22 +85,21 @@ __device__ __forceinline__ void flush(Lane8 (&s)[V], float* out, int cols, int y
 // A worker's rows in steps of the block's row count, none of which crosses
 // from one gate row's tokens into the next's.
 struct Steps {
-    int64_t at, hi, end, per, gate;
-    int rows;
+    int at, hi, end, per, gate, rows;
     __device__ __forceinline__ Steps(const BlockBwd& p, int rows_cta) {
-        const Span s = worker_rows(blockIdx.x, p.rows, p.workers);
-        at = s.lo;
-        end = s.hi;
-        per = p.rows_per_gate;
+        const Split s(p);
+        at = s.first(blockIdx.x);
+        end = s.first(blockIdx.x + 1);
+        per = (int)min(p.rows_per_gate, p.rows);   // (one gate row covers them all)
         rows = rows_cta;
         open();
     }
     __device__ __forceinline__ void open() {   // the gate row that `at` is in
         gate = per > 0 ? at / per : 0;
-        hi = per > 0 && (gate + 1) * per < end ? (gate + 1) * per : end;
+        hi = per > 0 && end - at > per - (at - gate * per) ? (gate + 1) * per : end;
     }
     __device__ __forceinline__ bool done() const { return at >= end; }
-    __device__ __forceinline__ bool last() const { return at + rows >= hi; }   // of this gate row
+    __device__ __forceinline__ bool last() const { return hi - at <= rows; }   // of this gate row
     __device__ __forceinline__ void next() {
         if (last()) {
             at = hi;
@@ -532,107 +539,101 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) block_bwd(const Blo
     flush_worker<true, FULL, V>(p, C, E, y, rows_cta, rw, reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
 }
 
-// The column pass: a block takes 128 columns, four a thread of a warp, its 16
+// The column pass: a block takes 64 columns, two a thread of a warp, its 16
 // warps share the partial sums of them.  blockIdx.y 0: dgamma_pre, dbeta_pre;
-// 1: dgamma_post, dbeta_post; from 2: the gate rows.
+// 1: dgamma_post, dbeta_post and, of a single gate row, dgate; from 2: the
+// gate rows, of several.
 constexpr int kColWarps = 16;
+constexpr int kColCols = 64;
 
-__device__ __forceinline__ void add4(float4& a, float4 b) {
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
-}
-__device__ __forceinline__ void fma4(float4& a, float4 w, float4 b) {
-    a.x = fmaf(w.x, b.x, a.x);
-    a.y = fmaf(w.y, b.y, a.y);
-    a.z = fmaf(w.z, b.z, a.z);
-    a.w = fmaf(w.w, b.w, a.w);
-}
-
-// The block's total of v, of column `threadIdx.x` (threads below 128).
-__device__ __forceinline__ float add_warps(float4 v, float4 (&sh)[kColWarps][32]) {
+// The block's totals of a and b, of column `threadIdx.x` (threads below 64).
+__device__ __forceinline__ float2 add_warps(float2 a, float2 b, float2 (&sh)[2][kColWarps][32]) {
     __syncthreads();
-    sh[threadIdx.x >> 5][threadIdx.x & 31] = v;
+    sh[0][threadIdx.x >> 5][threadIdx.x & 31] = a;
+    sh[1][threadIdx.x >> 5][threadIdx.x & 31] = b;
     __syncthreads();
-    float t = 0.f;
-    if (threadIdx.x < 128)
+    float2 t = both(0.f);
+    if (threadIdx.x < kColCols)
 #pragma unroll
-        for (int w = 0; w < kColWarps; ++w) t += reinterpret_cast<const float*>(sh[w])[threadIdx.x];
+        for (int w = 0; w < kColWarps; ++w) {
+            t.x += reinterpret_cast<const float*>(sh[0][w])[threadIdx.x];
+            t.y += reinterpret_cast<const float*>(sh[1][w])[threadIdx.x];
+        }
     return t;
 }
 
 __global__ void __launch_bounds__(32 * kColWarps) block_bwd_columns(const BlockBwd p) {
-    __shared__ float4 sh[kColWarps][32];
+    __shared__ float2 sh[2][kColWarps][32];
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
     const int64_t W = work_cols(p.cols);
-    const int64_t c = (int64_t)blockIdx.x * 128 + 4 * l;          // columns this thread reads
-    const int64_t co = (int64_t)blockIdx.x * 128 + threadIdx.x;   // column it writes
-    const bool in = c < W, out = co < p.cols && threadIdx.x < 128;
+    const int c = blockIdx.x * kColCols + 2 * l;          // columns this thread reads
+    const int co = blockIdx.x * kColCols + threadIdx.x;   // column it writes
+    const bool in = c < W, out = co < p.cols && threadIdx.x < kColCols;
     const int64_t slots = block_bwd_slots(p.workers, p.gates);
     const float* A = p.work + c;
     const float* B = A + slots * W;
     const float* C = B + slots * W;
     const float* E = C + p.workers * W;
-    const int64_t P = p.rows > 0 ? p.workers : 0;
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 a = none, b = none;
-    auto row = [&](const float* base, int64_t i) { return __ldcs(reinterpret_cast<const float4*>(base + i * W)); };
+    const int P = p.rows > 0 ? (int)p.workers : 0;
+    float2 a = both(0.f), b = both(0.f);
+    auto row = [&](const float* base, int64_t i) { return __ldcs(reinterpret_cast<const float2*>(base + i * W)); };
+    // the sum of partial rows [lo, hi), every kColWarps-th of them a warp's
+    auto add_rows = [&](const float* base, int lo, int hi) {
+        float2 t = both(0.f);
+        if (in)
+#pragma unroll 8
+            for (int i = lo + w; i < hi; i += kColWarps) t = add2(t, row(base, i));
+        return t;
+    };
+    const bool one_gate = p.gates == 1;
     if (blockIdx.y == 0) {
-        if (in) {
-            if (p.dgamma_pre)
-#pragma unroll 4
-                for (int64_t i = w; i < P; i += kColWarps) add4(a, row(C, i));
-            if (p.dbeta_pre)
-#pragma unroll 4
-                for (int64_t i = w; i < P; i += kColWarps) add4(b, row(E, i));
+        if (p.dgamma_pre) a = add_rows(C, 0, P);
+        if (p.dbeta_pre) b = add_rows(E, 0, P);
+        const float2 t = add_warps(a, b, sh);
+        if (out && p.dgamma_pre) p.dgamma_pre[co] = t.x;
+        if (out && p.dbeta_pre) p.dbeta_pre[co] = t.y;
+    } else if (blockIdx.y == 1 && one_gate) {
+        a = add_rows(A, 0, P);
+        if (p.dbeta_post || (p.dgate && p.beta_post)) b = add_rows(B, 0, P);
+        const float2 t = add_warps(a, b, sh);
+        if (out) {
+            const float gate = p.gate ? p.gate[co] : 1.f;
+            if (p.dgamma_post) p.dgamma_post[co] = gate * t.x;
+            if (p.dbeta_post) p.dbeta_post[co] = gate * t.y;
+            if (p.dgate)
+                p.dgate[co] = fmaf(p.gamma_post ? p.gamma_post[co] : 1.f, t.x,
+                                   p.beta_post ? p.beta_post[co] * t.y : 0.f);
         }
-        const float ta = add_warps(a, sh), tb = add_warps(b, sh);
-        if (out && p.dgamma_pre) p.dgamma_pre[co] = ta;
-        if (out && p.dbeta_pre) p.dbeta_pre[co] = tb;
     } else if (blockIdx.y == 1) {
-        for (int64_t i = w; i < P && in; i += kColWarps) {
-            const Span r = worker_rows(i, p.rows, p.workers);
-            const int64_t g0 = p.rows_per_gate > 0 ? r.lo / p.rows_per_gate : 0;
-            const int64_t g1 = p.rows_per_gate > 0 ? (r.hi - 1) / p.rows_per_gate : 0;
-            for (int64_t g = g0; g <= g1; ++g) {
-                float4 gt = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (p.gate) {
-                    const float* q = p.gate + g * p.cols + c;
-                    gt.x = __ldg(q);
-                    gt.y = c + 1 < p.cols ? __ldg(q + 1) : 0.f;
-                    gt.z = c + 2 < p.cols ? __ldg(q + 2) : 0.f;
-                    gt.w = c + 3 < p.cols ? __ldg(q + 3) : 0.f;
+        if (in && P > 0 && (p.dgamma_post || p.dbeta_post)) {
+            const Split s(p);
+            const int per = (int)p.rows_per_gate;
+            for (int i = w; i < P; i += kColWarps) {
+                const int g1 = (s.first(i + 1) - 1) / per;
+                for (int g = s.first(i) / per; g <= g1; ++g) {
+                    const float* q = p.gate + (int64_t)g * p.cols + c;   // (several gate rows: there is a gate)
+                    const float2 gt = make_float2(c < p.cols ? __ldg(q) : 0.f, c + 1 < p.cols ? __ldg(q + 1) : 0.f);
+                    if (p.dgamma_post) a = fma2(gt, row(A, i + g), a);
+                    if (p.dbeta_post) b = fma2(gt, row(B, i + g), b);
                 }
-                if (p.dgamma_post) fma4(a, gt, row(A, i + g));
-                if (p.dbeta_post) fma4(b, gt, row(B, i + g));
             }
         }
-        const float ta = add_warps(a, sh), tb = add_warps(b, sh);
-        if (out && p.dgamma_post) p.dgamma_post[co] = ta;
-        if (out && p.dbeta_post) p.dbeta_post[co] = tb;
+        const float2 t = add_warps(a, b, sh);
+        if (out && p.dgamma_post) p.dgamma_post[co] = t.x;
+        if (out && p.dbeta_post) p.dbeta_post[co] = t.y;
     } else {
+        const int per = (int)p.rows_per_gate;
+        const Split s(p);
         for (int64_t g = blockIdx.y - 2; g < p.gates; g += gridDim.y - 2) {
-            a = b = none;
-            if (P > 0 && in) {
-                const int64_t lo = p.rows_per_gate > 0 ? g * p.rows_per_gate : 0;
-                int64_t hi = p.rows_per_gate > 0 ? lo + p.rows_per_gate : p.rows;
-                if (hi > p.rows) hi = p.rows;
-                // the workers that hold rows lo and hi - 1
-                int64_t w0 = lo * P / p.rows, w1 = (hi - 1) * P / p.rows;
-                while (worker_rows(w0, p.rows, P).hi <= lo) ++w0;
-                while (worker_rows(w1, p.rows, P).hi < hi) ++w1;
-                for (int64_t i = w0 + w; i <= w1; i += kColWarps) {
-                    add4(a, row(A, i + g));
-                    if (p.beta_post) add4(b, row(B, i + g));
-                }
-            }
-            const float ta = add_warps(a, sh), tb = add_warps(b, sh);
-            if (out) {
-                const float ga = p.gamma_post ? p.gamma_post[co] : 1.f;
-                const float be = p.beta_post ? p.beta_post[co] : 0.f;
-                p.dgate[g * p.cols + co] = fmaf(ga, ta, be * tb);
-            }
+            const int64_t lo = g * per, hi = min(lo + per, p.rows);
+            // partial rows of the workers that hold rows lo .. hi - 1
+            const int w0 = s.worker((int)lo), w1 = s.worker((int)(hi - 1)) + 1;
+            a = add_rows(A + g * W, w0, w1);
+            if (p.beta_post) b = add_rows(B + g * W, w0, w1);
+            const float2 t = add_warps(a, b, sh);
+            if (out)
+                p.dgate[g * p.cols + co] = fmaf(p.gamma_post ? p.gamma_post[co] : 1.f, t.x,
+                                                p.beta_post ? p.beta_post[co] * t.y : 0.f);
         }
     }
 }
@@ -698,8 +699,9 @@ cudaError_t by_format(const BlockBwd& a, bool vec, bool codes, cudaStream_t s) {
 
 }  // namespace
 
-int64_t block_bwd_workers(int64_t rows, int64_t) {
-    return rows < 1 ? 1 : rows < kBwdCtas ? rows : kBwdCtas;
+int64_t block_bwd_workers(int64_t rows, int64_t cols) {
+    const int64_t most = most_workers(cols);
+    return rows < 1 ? 1 : rows < most ? rows : most;
 }
 
 cudaError_t block_backward(const BlockBwd& a, int dtype, bool codes, cudaStream_t s, int) {
@@ -713,8 +715,8 @@ cudaError_t block_backward(const BlockBwd& a, int dtype, bool codes, cudaStream_
     }
     const bool pre = a.dgamma_pre || a.dbeta_pre, post = a.dgamma_post || a.dbeta_post;
     if (!pre && !post && !a.dgate) return cudaSuccess;
-    const int64_t gates = a.dgate ? (a.gates < 4096 ? a.gates : 4096) : 0;
-    const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)(2 + gates));
+    const int64_t gates = a.dgate && a.gates > 1 ? (a.gates < 4096 ? a.gates : 4096) : 0;
+    const dim3 grid((unsigned)((a.cols + kColCols - 1) / kColCols), (unsigned)(2 + gates));
     block_bwd_columns<<<grid, 32 * kColWarps, 0, s>>>(a);
     count_launches(1);
     return cudaGetLastError();

@@ -54,7 +54,8 @@ struct BlockBwd {
 
 // CTAs of the backward's row pass, and the partial-sum rows of `cols` floats
 // they need: two a worker (dn*xhat, dn) and two a (worker, gate row) pair
-// (t*uhat, t).  Worker w takes rows [w*rows/workers, (w+1)*rows/workers).
+// (t*uhat, t), the pair (w, g) in slot w + g: workers take consecutive rows,
+// so from pair to pair at least one of the two grows.
 int64_t block_bwd_workers(int64_t rows, int64_t cols);
 __host__ __device__ inline int64_t block_bwd_slots(int64_t workers, int64_t gates) { return workers + gates; }
 
