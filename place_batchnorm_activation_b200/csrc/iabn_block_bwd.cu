@@ -23,9 +23,8 @@ void count_launches(int n);
 
 namespace {
 
-// Workers of the row pass at most: one wave of its blocks on 148 SMs, two a
-// SM up to 4096 columns (256 threads each), one above.
-inline int64_t most_workers(int64_t cols) { return cols <= 4096 ? 296 : 148; }
+constexpr int kBwdWarps = 8;      // of a row in one block
+constexpr int kBwdThreads = 128;  // a block's least threads (several rows, if need be)
 
 // Worker w's rows: rows / workers of them, one more for the first rows %
 // workers.  (32 bits: there are fewer than 2^31 rows.)
@@ -43,11 +42,12 @@ struct Split {
 // Columns as workspace rows hold them: whole 16-byte vectors.
 __host__ __device__ inline int64_t work_cols(int64_t cols) { return (cols + 3) / 4 * 4; }
 
-// Adds a block's rows (`rows` of them, this one being y) and writes one
-// partial-sum row; s starts again from zero.  The whole block calls it.
+// Adds the rows of a block and writes one partial-sum row; s starts again from
+// zero.  The whole block calls it.
 template <bool VEC, int V, class RW>
-__device__ __forceinline__ void flush(Lane8 (&s)[V], float* out, int cols, int y, int rows,
-                                      const RW& rw, float* columns) {
+__device__ __forceinline__ void flush(Lane8 (&s)[V], float* out, int cols, const RW& rw,
+                                      float* columns) {
+    const int y = rw.y, rows = rw.rows;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int c0 = (rw.w * V + k) * kSeg, left = cols - c0;
@@ -86,10 +86,10 @@ __device__ __forceinline__ void flush(Lane8 (&s)[V], float* out, int cols, int y
 // from one gate row's tokens into the next's.
 struct Steps {
     int at, hi, end, per, gate, rows;
-    __device__ __forceinline__ Steps(const BlockBwd& p, int rows_cta) {
+    __device__ __forceinline__ Steps(const BlockBwd& p, int worker, int rows_cta) {
         const Split s(p);
-        at = s.first(blockIdx.x);
-        end = s.first(blockIdx.x + 1);
+        at = s.first(worker);
+        end = s.first(worker + 1);
         per = (int)min(p.rows_per_gate, p.rows);   // (one gate row covers them all)
         rows = rows_cta;
         open();
@@ -122,6 +122,7 @@ __device__ __forceinline__ void zero(Lane8 (&s)[V]) {
 // norm's mean would have moved them.
 template <bool VEC>
 __device__ __forceinline__ void mask8(Lane8& f, int lane, int left) {
+    if (left >= kSeg) return;   // (the same for the whole warp)
 #pragma unroll
     for (int j = 0; j < kEl; ++j)
         if (seg_col<VEC>(lane, j) >= left) el(f, j) = 0.f;
@@ -211,30 +212,32 @@ __device__ __forceinline__ void load_weight(const float* gamma, const float* gat
 // The sums of a finished gate row, and of a finished worker.
 template <bool VEC, bool FULL, int V, class RW>
 __device__ __forceinline__ void flush_gate(const BlockBwd& p, int64_t gate, Lane8 (&A)[V],
-                                           Lane8 (&B)[V], int y, int rows, const RW& rw, float* columns) {
+                                           Lane8 (&B)[V], const RW& rw, float* columns) {
     const int64_t W = work_cols(p.cols), slots = block_bwd_slots(p.workers, p.gates);
-    const int64_t slot = blockIdx.x + gate;
-    flush<VEC, V>(A, p.work + slot * W, p.cols, y, rows, rw, columns);
-    if (FULL) flush<VEC, V>(B, p.work + (slots + slot) * W, p.cols, y, rows, rw, columns);
+    const int64_t slot = rw.block + gate;
+    flush<VEC, V>(A, p.work + slot * W, p.cols, rw, columns);
+    if (FULL) flush<VEC, V>(B, p.work + (slots + slot) * W, p.cols, rw, columns);
 }
 template <bool VEC, bool FULL, int V, class RW>
-__device__ __forceinline__ void flush_worker(const BlockBwd& p, Lane8 (&C)[V], Lane8 (&E)[V], int y,
-                                             int rows, const RW& rw, float* columns) {
+__device__ __forceinline__ void flush_worker(const BlockBwd& p, Lane8 (&C)[V], Lane8 (&E)[V],
+                                             const RW& rw, float* columns) {
     const int64_t W = work_cols(p.cols), slots = block_bwd_slots(p.workers, p.gates);
-    flush<VEC, V>(C, p.work + (2 * slots + blockIdx.x) * W, p.cols, y, rows, rw, columns);
+    flush<VEC, V>(C, p.work + (2 * slots + rw.block) * W, p.cols, rw, columns);
     if (FULL)
-        flush<VEC, V>(E, p.work + (2 * slots + p.workers + blockIdx.x) * W, p.cols, y, rows, rw, columns);
+        flush<VEC, V>(E, p.work + (2 * slots + p.workers + rw.block) * W, p.cols, rw, columns);
 }
 
 // Any width and alignment: each row is loaded as its turn comes.
-template <int DT, bool VEC, int V, int FMT>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_bwd_any(const BlockBwd p, int row_warps) {
+constexpr int kAnyV = 2;   // segments a warp
+
+template <int DT, int V, int FMT, bool CLUSTER>
+__global__ void __launch_bounds__(256, 2) block_bwd_any(const BlockBwd p, int row_warps) {
     using T = typename Storage<DT>::T;
-    extern __shared__ float4 shared[];   // sums of a row, then (several rows a block) of columns
-    const int rows_cta = (blockDim.x >> 5) / row_warps;
-    RowWarps<V == 4 ? 32 : 16> rw(row_warps, reinterpret_cast<float*>(shared));
-    const int y = rw.bar - 1;
-    float* columns = reinterpret_cast<float*>(shared) + rows_cta * kRowFloats;
+    constexpr bool VEC = false;
+    extern __shared__ float4 shared[];   // several rows a block: their sums of columns
+    __shared__ __align__(16) float red[kRedFloats];
+    RowWarps<CLUSTER> rw(row_warps, red);
+    float* columns = reinterpret_cast<float*>(shared);
     const float inv_n = 1.f / (float)p.cols;
     const int64_t D = p.cols;
     const int c0 = rw.w * V * kSeg;
@@ -261,8 +264,8 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_bwd_any(const Bl
             mask8<VEC>(f, rw.lane, left);
         }
     };
-    for (Steps st(p, rows_cta); !st.done(); st.next()) {
-        const int64_t row = st.at + y;
+    for (Steps st(p, rw.block, rw.rows); !st.done(); st.next()) {
+        const int64_t row = st.at + rw.y;
         if (row < st.hi) {
             Lane8 t[V], x[V];
             zero(t);
@@ -324,18 +327,16 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_bwd_any(const Bl
                     store8<DT, VEC>(static_cast<T*>(p.du) + row * D + c0 + k * kSeg, rw.lane,
                                     p.cols - c0 - k * kSeg, t[k]);
         }
-        if (st.last()) flush_gate<VEC, true, V>(p, st.gate, A, B, y, rows_cta, rw, columns);
+        if (st.last()) flush_gate<VEC, true, V>(p, st.gate, A, B, rw, columns);
     }
-    flush_worker<VEC, true, V>(p, C, E, y, rows_cta, rw, columns);
+    flush_worker<VEC, true, V>(p, C, E, rw, columns);
+    rw.end();
 }
 
-// VEC widths up to 8192: a thread copies its share of the rows to come into a
+// VEC: a thread copies its share of the rows to come into a
 // ring of its own, two rows ahead, dn and xhat in one group of copies, dh' and
 // uhat in the next: each half of a slot is filled again as soon as the thread
 // has read it.
-constexpr int kBwdV = 2;          // segments a warp
-constexpr int kBwdThreads = 256;  // a block's least threads (several rows, if need be)
-
 // Shared memory of a thread, in 16-byte quads: gate*gamma_post and gamma_pre,
 // and two slots of two halves: a gradient (dn | dh') and what was kept (xhat |
 // uhat).
@@ -356,17 +357,16 @@ struct Scalars {
     float rstd, mean, scale[V];
 };
 
-template <int DT, int V, int FMT, bool FULL, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) block_bwd(const BlockBwd p, int row_warps) {
+template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+__global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const BlockBwd p, int row_warps) {
     using T = typename Storage<DT>::T;
     using S = BwdShared<DT, V, FMT>;
     constexpr int Q = S::Q;
     constexpr bool CODES = FMT != kNoCodes;
     extern __shared__ float4 shared[];
-    __shared__ __align__(16) float red[8 * kRowFloats];
-    const int rows_cta = (blockDim.x >> 5) / row_warps;
-    RowWarps<MAXT / 32> rw(row_warps, red);
-    const int y = rw.bar - 1;
+    __shared__ __align__(16) float red[kRedFloats];
+    RowWarps<CLUSTER> rw(row_warps, red);
+    const int y = rw.y;
     float4* mine = shared + threadIdx.x;   // quad i of the thread: mine[i * blockDim.x]
     const float inv_n = 1.f / (float)p.cols;
     const int c0 = rw.w * V * kSeg;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) block_bwd(const Blo
         }
     };
 
-    Steps st(p, rows_cta), ahead(p, rows_cta);
+    Steps st(p, rw.block, rw.rows), ahead(p, rw.block, rw.rows);
     auto fetch_next = [&](int slot, int half) { fetch(slot, half, ahead.at + y, !ahead.done() && ahead.at + y < ahead.hi); };
     fetch_next(0, 0);
     fetch_next(0, 1);
@@ -539,14 +539,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) block_bwd(const Blo
         }
         const bool last = st.last();
         if (last)   // (behind the ring and the coefficients: the rows' sums of columns)
-            flush_gate<true, FULL, V>(p, st.gate, A, B, y, rows_cta, rw,
+            flush_gate<true, FULL, V>(p, st.gate, A, B, rw,
                                       reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
         st.next();
         if (last && p.gate && p.rows_per_gate > 0 && !st.done())
             set_coef(0, p.gamma_post, p.gate + st.gate * p.cols);
     }
     copies_wait<0>();
-    flush_worker<true, FULL, V>(p, C, E, y, rows_cta, rw, reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+    flush_worker<true, FULL, V>(p, C, E, rw, reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+    rw.end();
 }
 
 // The column pass: a block takes 64 columns, two a thread of a warp, its 16
@@ -648,57 +649,52 @@ __global__ void __launch_bounds__(32 * kColWarps) block_bwd_columns(const BlockB
     }
 }
 
-template <int DT, bool VEC, int FMT, int V>
-cudaError_t launch_any(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
-    const int threads = 32 * row_warps * rows_cta;
-    const size_t smem = (rows_cta * kRowFloats + (rows_cta > 1 ? threads / 32 * kSeg : 0)) * sizeof(float);
-    block_bwd_any<DT, VEC, V, FMT><<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
-    count_launches(1);
-    return cudaGetLastError();
+// Shared memory for the sums of columns of a block's rows.
+size_t columns_bytes(const RowShape& s) {
+    return s.rows > 1 ? s.rows * s.warps * kSeg * sizeof(float) : 0;
 }
 
-constexpr size_t kMostShared = 227 * 1024 - 8 * kRowFloats * sizeof(float);
-
-template <int DT, int FMT>
-size_t shared_bytes(int threads, int rows_cta) {
-    return (size_t)BwdShared<DT, kBwdV, FMT>::kQuads * 16 * threads +
-           (rows_cta > 1 ? threads / 32 * kSeg * sizeof(float) : 0);
+template <int DT, int FMT, bool CLUSTER>
+cudaError_t launch_any(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
+    return launch_rows(block_bwd_any<DT, kAnyV, FMT, CLUSTER>, s, a.workers, columns_bytes(s), stream, a);
 }
 
-template <int DT, int FMT, bool FULL>
-cudaError_t launch(const BlockBwd& a, int row_warps, int rows_cta, cudaStream_t s) {
-    const int threads = 32 * row_warps * rows_cta;
-    const size_t smem = shared_bytes<DT, FMT>(threads, rows_cta);
-    auto kernel = threads <= 256 ? block_bwd<DT, kBwdV, FMT, FULL, 256> : block_bwd<DT, kBwdV, FMT, FULL, 512>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)a.workers, threads, smem, s>>>(a, row_warps);
-    count_launches(1);
-    return cudaGetLastError();
+template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+cudaError_t launch(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
+    const size_t smem = (size_t)BwdShared<DT, V, FMT>::kQuads * 16 * s.threads() + columns_bytes(s);
+    return launch_rows(block_bwd<DT, V, FMT, FULL, CLUSTER>, s, a.workers, smem, stream, a);
 }
 
-template <int DT, int FMT>
-cudaError_t by_width(const BlockBwd& a, bool vec, cudaStream_t s) {
-    const int segs = (a.cols + kSeg - 1) / kSeg;
-    if (vec && segs <= 32) {
-        const int row_warps = (segs + kBwdV - 1) / kBwdV;
-        const int rows_cta = row_warps * 32 >= kBwdThreads ? 1 : kBwdThreads / 32 / row_warps;
-        if (shared_bytes<DT, FMT>(32 * row_warps * rows_cta, rows_cta) <= kMostShared) {
-            const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.dbeta_post || a.dbeta_pre ||
-                              (a.dgate && a.beta_post);
-            return full ? launch<DT, FMT, true>(a, row_warps, rows_cta, s)
-                        : launch<DT, FMT, false>(a, row_warps, rows_cta, s);
-        }
+template <int DT, int V, int FMT>
+cudaError_t by_shape(const BlockBwd& a, bool full, cudaStream_t stream) {
+    const RowShape s = RowShape::of<V>(a.cols, V == 4 ? kBwdThreads : 2 * kBwdThreads, kBwdWarps);
+    if constexpr (V == 4 || (DT == kF32 && FMT == kNoCodes)) {
+        if (s.cluster > 1)
+            return full ? launch<DT, V, FMT, true, true>(a, s, stream)
+                        : launch<DT, V, FMT, false, true>(a, s, stream);
     }
-    if (segs <= 16) {
-        const int rows_cta = segs >= 8 ? 1 : 8 / segs;
-        return vec ? launch_any<DT, true, FMT, 1>(a, segs, rows_cta, s)
-                   : launch_any<DT, false, FMT, 1>(a, segs, rows_cta, s);
+    return full ? launch<DT, V, FMT, true, false>(a, s, stream) : launch<DT, V, FMT, false, false>(a, s, stream);
+}
+
+// Segments a warp, by measurement (bf16 from e4m3): with all four sums of
+// columns (FULL) two segments leave 54 registers spilled at two blocks an SM,
+// four keep everything in registers (16384 x 4096: 261 and 162 us; x 2048: 144
+// and 92); with two sums both fit, and two segments are as fast up to 4096
+// columns (16384 x 4096: 130 and 132 us; x 1024: 41 and 44), while above four
+// keep a row in one block (8192 x 8192: 196 us with a cluster of two, 143).
+template <int DT, int FMT>
+cudaError_t by_width(const BlockBwd& a, bool vec, cudaStream_t stream) {
+    count_launches(1);
+    const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.dbeta_post || a.dbeta_pre ||
+                      (a.dgate && a.beta_post);
+    if (!vec) {
+        const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kBwdWarps);
+        return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream) : launch_any<DT, FMT, false>(a, s, stream);
     }
-    if (segs <= 32) return vec ? launch_any<DT, true, FMT, 2>(a, (segs + 1) / 2, 1, s)
-                               : launch_any<DT, false, FMT, 2>(a, (segs + 1) / 2, 1, s);
-    return vec ? launch_any<DT, true, FMT, 4>(a, (segs + 3) / 4, 1, s)
-               : launch_any<DT, false, FMT, 4>(a, (segs + 3) / 4, 1, s);
+    // (kept fp32 tensors of wider rows exceed a block's shared memory with four)
+    constexpr bool kWide = DT == kF32 && FMT == kNoCodes;
+    if (a.cols > (full ? 2 * kSeg : 4096) && !(kWide && a.cols > 4096)) return by_shape<DT, 4, FMT>(a, full, stream);
+    return by_shape<DT, 2, FMT>(a, full, stream);
 }
 
 template <int DT>
@@ -709,8 +705,10 @@ cudaError_t by_format(const BlockBwd& a, bool vec, bool codes, cudaStream_t s) {
 
 }  // namespace
 
+// One wave of the row pass's blocks on 148 SMs: two a SM up to 4096 columns,
+// one above, where clusters of them share rows of more than 8192.
 int64_t block_bwd_workers(int64_t rows, int64_t cols) {
-    const int64_t most = most_workers(cols);
+    const int64_t most = cols <= 4096 ? 296 : 148 / RowShape::of<4>((int)cols, kBwdThreads, kBwdWarps).cluster;
     return rows < 1 ? 1 : rows < most ? rows : most;
 }
 

@@ -6,8 +6,7 @@
 //   xhat = pre(h');  n = gamma_pre xhat + beta_pre.
 //
 // A row is held in registers between its two reductions, eight columns a lane
-// and segment; LAYER's variance is the mean square about the mean already
-// known (two reductions), so it does not cancel for rows far from zero.
+// and segment.
 // Bound: HBM bandwidth, 4 s bytes an element (s the storage size), 2 more
 // with checkpoints.
 #include "iabn_rows.cuh"
@@ -19,25 +18,52 @@ void count_launches(int n);
 namespace {
 
 // Statistics of one row held as V segments; v becomes the normalised row.
-// FULL: the norm may be LAYER.
+// FULL: the norm may be LAYER.  Its variance is the mean square about a mean
+// that is already known, so it does not cancel for rows far from zero: about
+// the warp's own mean first, and between the warps' means once they have been
+// exchanged with those sums (one barrier for both).
 template <bool VEC, bool FULL, int V, class RW>
 __device__ __forceinline__ void norm_row(Lane8 (&v)[V], int kind, int c0, int cols, float eps, RW& rw,
                                          float& mean, float& rstd) {
     const float inv_n = 1.f / (float)cols;
-    mean = 0.f;
     if (FULL && kind == kNormLayer) {
-        float2 s = both(0.f);
+        const int left = cols - c0;   // the warp's columns, if below V kSeg
+        float2 s = both(0.f), q = both(0.f);
 #pragma unroll
         for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int j = 0; j < kEl / 2; ++j) s = add2(s, v[k][j]);
-        mean = rw.sum(s) * inv_n;
+        const float own = left > 0 ? rw.warp_total(s) / (float)min(left, V * kSeg) : 0.f;
+        auto mask = [&]() {   // past the row's end v stays zero
+            if (left < V * kSeg)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+#pragma unroll
+                    for (int j = 0; j < kEl; ++j)
+                        if (k * kSeg + seg_col<VEC>(rw.lane, j) >= left) el(v[k], j) = 0.f;
+        };
 #pragma unroll
         for (int k = 0; k < V; ++k)
 #pragma unroll
-            for (int j = 0; j < kEl; ++j)
-                el(v[k], j) = c0 + k * kSeg + seg_col<VEC>(rw.lane, j) < cols ? el(v[k], j) - mean : 0.f;
+            for (int j = 0; j < kEl / 2; ++j) v[k][j] = add2(v[k][j], both(-own));
+        mask();
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int j = 0; j < kEl / 2; ++j) q = fma2(v[k][j], v[k][j], q);
+        float square = rw.warp_total(q);
+        mean = own;
+        rw.template merge<V * kSeg>(mean, square, cols, inv_n);
+        rstd = rsqrtf(fmaf(square, inv_n, eps));
+        const float shift = (own - mean) * rstd;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int j = 0; j < kEl / 2; ++j) v[k][j] = fma2(v[k][j], both(rstd), both(shift));
+        mask();
+        return;
     }
+    mean = 0.f;
     float2 q = both(0.f);
 #pragma unroll
     for (int k = 0; k < V; ++k)
@@ -56,7 +82,11 @@ __device__ __forceinline__ const float* gate_of(const BlockFwd& p, int64_t row) 
     return p.gate + row / p.rows_per_gate * p.cols;
 }
 
-// gate*gamma_post (which = 0) or gamma_pre (1) of segment k, from the parameters.
+// What goes by column and stays the same from row to row.
+enum : int { kScalePost = 0, kScalePre = 1, kShiftPost = 2, kShiftPre = 3 };
+
+// Those of segment k, from the parameters: gate*gamma_post, gamma_pre,
+// gate*beta_post, beta_pre.
 template <bool VEC, int V>
 struct Params {
     const BlockFwd& p;
@@ -64,8 +94,12 @@ struct Params {
     int c0, lane;
     __device__ __forceinline__ void get(int which, int k, Lane8& f) const {
         const int c = c0 + k * kSeg, left = p.cols - c;
-        load_param<VEC>(which == 0 ? p.gamma_post : p.gamma_pre, c, lane, left, 1.f, f);
-        if (which == 0 && gate) {
+        const float* from = which == kScalePost   ? p.gamma_post
+                            : which == kScalePre  ? p.gamma_pre
+                            : which == kShiftPost ? p.beta_post
+                                                  : p.beta_pre;
+        load_param<VEC>(from, c, lane, left, which < kShiftPost ? 1.f : 0.f, f);
+        if ((which == kScalePost || which == kShiftPost) && gate) {
             Lane8 g;
             load_param<VEC>(gate, c, lane, left, 1.f, g);
 #pragma unroll
@@ -74,12 +108,13 @@ struct Params {
     }
 };
 
-// The same kept in the thread's own part of shared memory, 16 bytes at a time,
-// while it stays the same from row to row.  (Registers would hold it too, but
-// these 16 V cost a third of the warps.)
-template <int V>
+// The same kept in the thread's own part of shared memory, 16 bytes at a time.
+// (In registers they would cost a third of the warps; read for every row, they
+// miss the L1 that is left and double the traffic to L2: 16384 x 4096 layer
+// norms with shifts 188 us.)  FULL: with the shifts.
+template <int V, bool FULL>
 struct Coef {
-    static constexpr int kQuads = 2 * V * 2;   // a thread's
+    static constexpr int kQuads = (FULL ? 4 : 2) * V * 2;   // a thread's
     float4* mine;   // [which][segment][half] x blockDim
     __device__ __forceinline__ void get(int which, int k, Lane8& f) const {
 #pragma unroll
@@ -103,8 +138,7 @@ struct Coef {
 };
 
 // One row, held as V segments: x holds u (if has_u), h the residual stream.
-// c: what goes by column (the shifts are read here).  FULL: there may be LAYER
-// norms and shifts.
+// c: what goes by column.  FULL: there may be LAYER norms and shifts.
 template <int DT, bool VEC, bool FULL, int V, int FMT, class C, class RW>
 __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool has_u,
                                           int c0, const C& c, Lane8 (&x)[V], Lane8 (&h)[V],
@@ -128,15 +162,15 @@ __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool h
         for (int k = 0; k < V; ++k) {
             const int col = c0 + k * kSeg, left = p.cols - col;
             Lane8 ga;
-            c.get(0, k, ga);
-#pragma unroll
-            for (int j = 0; j < kEl / 2; ++j) x[k][j] = mul2(x[k][j], ga[j]);
+            c.get(kScalePost, k, ga);
             if (FULL && p.beta_post) {
-                Lane8 g, be;
-                load_param<VEC>(gate_of(p, row), col, rw.lane, left, 1.f, g);
-                load_param<VEC>(p.beta_post, col, rw.lane, left, 0.f, be);
+                Lane8 be;
+                c.get(kShiftPost, k, be);
 #pragma unroll
-                for (int j = 0; j < kEl / 2; ++j) x[k][j] = fma2(g[j], be[j], x[k][j]);
+                for (int j = 0; j < kEl / 2; ++j) x[k][j] = fma2(x[k][j], ga[j], be[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kEl / 2; ++j) x[k][j] = mul2(x[k][j], ga[j]);
             }
 #pragma unroll
             for (int j = 0; j < kEl / 2; ++j) h[k][j] = fma2(both(p.alpha), h[k][j], x[k][j]);
@@ -158,10 +192,10 @@ __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool h
     for (int k = 0; k < V; ++k) {
         const int col = c0 + k * kSeg, left = p.cols - col;
         Lane8 ga;
-        c.get(1, k, ga);
+        c.get(kScalePre, k, ga);
         if (FULL && p.beta_pre) {
             Lane8 be;
-            load_param<VEC>(p.beta_pre, col, rw.lane, left, 0.f, be);
+            c.get(kShiftPre, k, be);
 #pragma unroll
             for (int j = 0; j < kEl / 2; ++j) h[k][j] = fma2(ga[j], h[k][j], be[j]);
         } else {
@@ -173,20 +207,21 @@ __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool h
 }
 
 // Any width and alignment: each row is loaded as its turn comes.
-template <int DT, bool VEC, int V, int FMT>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_fwd_any(const BlockFwd p, int row_warps) {
+constexpr int kAnyV = 2;   // segments a warp
+
+template <int DT, int V, int FMT, bool CLUSTER>
+__global__ void __launch_bounds__(256) block_fwd_any(const BlockFwd p, int row_warps) {
     using T = typename Storage<DT>::T;
-    __shared__ __align__(16) float red[8 * kRowFloats];
-    RowWarps<V == 4 ? 32 : 16> rw(row_warps, red);
-    const int rows_cta = (blockDim.x >> 5) / row_warps;
+    __shared__ __align__(16) float red[kRedFloats];
+    RowWarps<CLUSTER> rw(row_warps, red);
     const T* U = static_cast<const T*>(p.u);
     const T* H = static_cast<const T*>(p.h);
     const int c0 = rw.w * V * kSeg;
-    for (int64_t row = (int64_t)blockIdx.x * rows_cta + rw.bar - 1; row < p.rows;
-         row += (int64_t)gridDim.x * rows_cta) {
+    const int64_t step = (int64_t)(gridDim.x / (CLUSTER ? cluster_size() : 1)) * rw.rows;
+    for (int64_t row = (int64_t)rw.block * rw.rows + rw.y; row < p.rows; row += step) {
         const int64_t at = row * p.cols;
         Lane8 x[V], h[V];
-        Raw<DT, VEC> ru[V], rh[V];
+        Raw<DT, false> ru[V], rh[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             if (U) ru[k].load(U + at + c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg);
@@ -197,38 +232,38 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512, 1) block_fwd_any(const Bl
             if (U) ru[k].get(x[k]);
             rh[k].get(h[k]);
         }
-        const Params<VEC, V> c{p, gate_of(p, row), c0, rw.lane};
-        block_row<DT, VEC, true, V, FMT>(p, row, U != nullptr, c0, c, x, h, rw);
+        const Params<false, V> c{p, gate_of(p, row), c0, rw.lane};
+        block_row<DT, false, true, V, FMT>(p, row, U != nullptr, c0, c, x, h, rw);
     }
+    rw.end();
 }
 
-// VEC widths up to 8192: a thread copies its share of the rows to come into a
+// VEC: a thread copies its share of the rows to come into a
 // ring of its own, kStages - 1 rows ahead.
 constexpr int kStages = 2;
-constexpr int kFwdV = 2;          // segments a warp
+constexpr int kFwdWarps = 8;      // of a row in one block
 constexpr int kFwdThreads = 256;  // a block's least threads (several rows, if need be)
 
-
-template <int DT, int V>
+template <int DT, int V, bool FULL>
 size_t shared_bytes(int threads) {
-    return ((size_t)kStages * 2 * V * Raw<DT, true>::kQuads + Coef<V>::kQuads) * 16 * threads;
+    return ((size_t)kStages * 2 * V * Raw<DT, true>::kQuads + Coef<V, FULL>::kQuads) * 16 * threads;
 }
 
-template <int DT, int V, int FMT, bool FULL, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) block_fwd(const BlockFwd p, int row_warps) {
+template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+__global__ void __launch_bounds__(256, V == 4 ? 1 : FULL ? 2 : 3) block_fwd(const BlockFwd p, int row_warps) {
     using T = typename Storage<DT>::T;
     constexpr int Q = Raw<DT, true>::kQuads;
     extern __shared__ uint4 shared[];
-    __shared__ __align__(16) float red[8 * kRowFloats];
-    RowWarps<MAXT / 32> rw(row_warps, red);
-    Coef<V> c{reinterpret_cast<float4*>(shared) + threadIdx.x};
-    uint4* ring = shared + Coef<V>::kQuads * blockDim.x + threadIdx.x;   // the thread's own
-    const int rows_cta = (blockDim.x >> 5) / row_warps;
+    __shared__ __align__(16) float red[kRedFloats];
+    RowWarps<CLUSTER> rw(row_warps, red);
+    Coef<V, FULL> c{reinterpret_cast<float4*>(shared) + threadIdx.x};
+    uint4* ring = shared + Coef<V, FULL>::kQuads * blockDim.x + threadIdx.x;   // the thread's own
     const bool has_u = p.u != nullptr;
     const int c0 = rw.w * V * kSeg;
     // a block takes consecutive rows, so that gate rows change seldom
-    const int64_t end = (blockIdx.x + 1) * p.rows / gridDim.x;
-    int64_t row = blockIdx.x * p.rows / gridDim.x + rw.bar - 1;
+    const int64_t blocks = gridDim.x / (CLUSTER ? cluster_size() : 1);
+    const int64_t end = (rw.block + 1) * p.rows / blocks;
+    int64_t row = rw.block * p.rows / blocks + rw.y;
     auto slot = [&](int stage, int tensor, int k, int i) {
         return ring + (((stage * 2 + tensor) * V + k) * Q + i) * blockDim.x;
     };
@@ -249,14 +284,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) block_fwd(const Blo
     // (what no copy writes, past the row's end and u where there is none, reads as zero)
     for (int i = 0; i < kStages * 2 * V * Q; ++i) ring[i * blockDim.x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(row + i * rows_cta, i);
-    c.set(1, Params<true, V>{p, nullptr, c0, rw.lane});
+    for (int i = 0; i < kStages - 1; ++i) fetch(row + i * rw.rows, i);
+    c.set(kScalePre, Params<true, V>{p, nullptr, c0, rw.lane});
+    if (FULL && p.beta_pre) c.set(kShiftPre, Params<true, V>{p, nullptr, c0, rw.lane});
     int64_t gate_end = -1;   // row at which another gate row begins
     int stage = 0;
-    for (; row < end; row += rows_cta) {
-        fetch(row + (kStages - 1) * rows_cta, stage == 0 ? kStages - 1 : stage - 1);
+    for (; row < end; row += rw.rows) {
+        fetch(row + (kStages - 1) * rw.rows, stage == 0 ? kStages - 1 : stage - 1);
         if (row >= gate_end && has_u) {
-            c.set(0, Params<true, V>{p, gate_of(p, row), c0, rw.lane});
+            const Params<true, V> from{p, gate_of(p, row), c0, rw.lane};
+            c.set(kScalePost, from);
+            if (FULL && p.beta_post) c.set(kShiftPost, from);
             gate_end = p.gate && p.rows_per_gate > 0 ? (row / p.rows_per_gate + 1) * p.rows_per_gate : end;
         }
         copies_wait<kStages - 1>();
@@ -276,45 +314,53 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) block_fwd(const Blo
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
+    rw.end();
 }
 
-template <int DT, bool VEC, int V, int FMT>
-cudaError_t launch_any(const BlockFwd& a, int row_warps, int rows_cta, cudaStream_t s, int sms) {
-    const int64_t need = (a.rows + rows_cta - 1) / rows_cta, most = (int64_t)sms * 32;
-    block_fwd_any<DT, VEC, V, FMT>
-        <<<(unsigned)(need < most ? need : most), 32 * row_warps * rows_cta, 0, s>>>(a, row_warps);
-    count_launches(1);
-    return cudaGetLastError();
+template <int DT, int FMT, bool CLUSTER>
+cudaError_t launch_any(const BlockFwd& a, const RowShape& s, cudaStream_t stream, int sms) {
+    const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * 32 / s.cluster;
+    return launch_rows(block_fwd_any<DT, kAnyV, FMT, CLUSTER>, s, need < most ? need : most, 0, stream, a);
 }
 
-template <int DT, int FMT, bool FULL>
-cudaError_t launch(const BlockFwd& a, int segs, cudaStream_t s, int sms) {
-    const int row_warps = (segs + kFwdV - 1) / kFwdV;
-    const int rows_cta = row_warps * 32 >= kFwdThreads ? 1 : kFwdThreads / 32 / row_warps;
-    const int threads = 32 * row_warps * rows_cta;
-    const size_t smem = shared_bytes<DT, kFwdV>(threads);
-    auto kernel = threads <= 256 ? block_fwd<DT, kFwdV, FMT, FULL, 256> : block_fwd<DT, kFwdV, FMT, FULL, 512>;
+template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+cudaError_t launch(const BlockFwd& a, const RowShape& s, cudaStream_t stream, int sms) {
+    const size_t smem = shared_bytes<DT, V, FULL>(s.threads());
+    auto kernel = block_fwd<DT, V, FMT, FULL, CLUSTER>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     int blocks = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, s.threads(), smem);
     if (e != cudaSuccess) return e;
-    const int64_t need = (a.rows + rows_cta - 1) / rows_cta, most = (int64_t)sms * blocks;
-    kernel<<<(unsigned)(need < most ? need : most), threads, smem, s>>>(a, row_warps);
-    count_launches(1);
-    return cudaGetLastError();
+    const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * blocks / s.cluster;
+    return launch_rows(kernel, s, need < most ? need : most, smem, stream, a);
 }
 
-template <int DT, int FMT>
-cudaError_t by_width(const BlockFwd& a, bool vec, cudaStream_t s, int sms) {
-    const int segs = (a.cols + kSeg - 1) / kSeg;
-    if (vec && segs <= 32) {
-        const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.beta_post || a.beta_pre;
-        return full ? launch<DT, FMT, true>(a, segs, s, sms) : launch<DT, FMT, false>(a, segs, s, sms);
+template <int DT, int V, int FMT>
+cudaError_t by_shape(const BlockFwd& a, bool full, cudaStream_t stream, int sms) {
+    const RowShape s = RowShape::of<V>(a.cols, kFwdThreads, kFwdWarps);
+    if constexpr (V == 4 || DT == kF32) {
+        if (s.cluster > 1)
+            return full ? launch<DT, V, FMT, true, true>(a, s, stream, sms)
+                        : launch<DT, V, FMT, false, true>(a, s, stream, sms);
     }
-    if (vec) return launch_any<DT, true, 4, FMT>(a, (segs + 3) / 4, 1, s, sms);
-    if (segs <= 16) return launch_any<DT, false, 1, FMT>(a, segs, segs >= 8 ? 1 : 8 / segs, s, sms);
-    if (segs <= 32) return launch_any<DT, false, 2, FMT>(a, (segs + 1) / 2, 1, s, sms);
-    return launch_any<DT, false, 4, FMT>(a, (segs + 3) / 4, 1, s, sms);
+    return full ? launch<DT, V, FMT, true, false>(a, s, stream, sms)
+                : launch<DT, V, FMT, false, false>(a, s, stream, sms);
+}
+
+// Segments a warp, by measurement: two up to 4096 columns (16384 x 4096 bf16,
+// e4m3: 119 us, with four 125), four above, which keep a row of up to 8192 in
+// one block (8192 x 8192: 129 us, 165 with two and a cluster of two blocks).
+// In fp32 four segments and the shifts exceed a block's shared memory: two.
+template <int DT, int FMT>
+cudaError_t by_width(const BlockFwd& a, bool vec, cudaStream_t stream, int sms) {
+    count_launches(1);
+    const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.beta_post || a.beta_pre;
+    if (vec && (a.cols <= 4096 || (DT == kF32 && full))) return by_shape<DT, 2, FMT>(a, full, stream, sms);
+    if (vec) return by_shape<DT, 4, FMT>(a, full, stream, sms);
+    const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kFwdWarps);
+    return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream, sms)
+                         : launch_any<DT, FMT, false>(a, s, stream, sms);
 }
 
 template <int DT>

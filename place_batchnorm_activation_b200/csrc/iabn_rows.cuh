@@ -450,30 +450,88 @@ __device__ __forceinline__ void quantise_row(const Lane8 (&f)[V], uint8_t* q, fl
 
 // ---------------------------------------------------------- sums over a row
 
-// The warps of one row: `n` of them, this one being `w`; `bar` their named
-// barrier, `red` 2 x 2 x 32 floats of shared memory, zero from n on.  A sum's
-// partials alternate between the two halves of `red`, so one barrier a sum is
-// enough: a half is written again only after the next sum's barrier, which
-// every warp passes after reading it.  The order of the additions is fixed.
-constexpr int kRowFloats = 128;
-template <int MOST>   // warps of a row at most
+// The warps of one row: `n` of them, this one being `w`.  Up to eight are in
+// one block, which then may hold several rows (this warp's is the block's y-th
+// of `rows`) with a named barrier each; where a row needs more, a cluster of
+// blocks shares it (CLUSTER), every warp's partial sums go to all of its
+// blocks' shared memory, and the cluster's barrier takes the named one's
+// place.  A sum's partials alternate between the two halves of `red`, so one
+// barrier a sum is enough: a half is written again only after the next sum's
+// barrier, which every warp passes after reading it.  The order of the
+// additions is fixed.
+constexpr int kRowWarps = 8;                       // of one block
+constexpr int kMaxCluster = 8;
+constexpr int kRedFloats = 2 * 2 * kRowWarps * kMaxCluster;   // `red` of a block
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p (in this block's shared memory) of block `rank` = v.
+__device__ __forceinline__ void store_in_block(float* p, uint32_t rank, float v) {
+    asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1;\n\t"
+                 "st.shared::cluster.f32 [a], %2; }" ::"r"((uint32_t)__cvta_generic_to_shared(p)),
+                 "r"(rank), "f"(v)
+                 : "memory");
+}
+
+template <bool CLUSTER>
 struct RowWarps {
-    int n, w, lane, bar;
+    int n, w, lane, y, rows, block;   // block: which of the grid's blocks or clusters
     float* red;
     int half;
-    // `all`: this block's kRowFloats floats for each of its rows.
-    __device__ __forceinline__ RowWarps(int row_warps, float* all) {
+    // warps: those of a row in one block.  `all`: kRedFloats floats.
+    __device__ __forceinline__ RowWarps(int warps, float* all) {
         const int warp = threadIdx.x >> 5;
-        const int y = warp / row_warps;
-        n = row_warps;
-        w = warp - y * row_warps;
         lane = threadIdx.x & 31;
-        bar = 1 + y;
-        red = all + y * kRowFloats;
+        rows = (blockDim.x >> 5) / warps;
+        y = warp / warps;
+        w = warp - y * warps;
+        n = warps;
+        block = blockIdx.x;
         half = 0;
-        if (w == 0)
-            for (int i = lane; i < kRowFloats; i += 32) red[i] = 0.f;
-        __syncthreads();
+        if (CLUSTER) {
+            w += cluster_rank() * warps;
+            n *= cluster_size();
+            block /= cluster_size();
+        }
+        red = all + y * (4 * kRowWarps);
+        for (int i = threadIdx.x; i < kRedFloats; i += blockDim.x) all[i] = 0.f;
+        if (CLUSTER) cluster_barrier();
+        else __syncthreads();
+    }
+    // The last thing that a block does: the others may still write to it.
+    __device__ __forceinline__ void end() const {
+        if (CLUSTER) cluster_barrier();
+    }
+    static constexpr int kMost = CLUSTER ? kRowWarps * kMaxCluster : kRowWarps;
+    // Puts every warp's v[i] at the returned r[i * kMost + warp].
+    template <int N>
+    __device__ __forceinline__ const float* exchange(const float (&v)[N]) {
+        float* r = red + half * (2 * kMost);
+        half ^= 1;
+        if (CLUSTER) {
+            if (lane < cluster_size())
+#pragma unroll
+                for (int i = 0; i < N; ++i) store_in_block(r + i * kMost + w, lane, v[i]);
+            cluster_barrier();
+        } else {
+            if (lane == 0)
+#pragma unroll
+                for (int i = 0; i < N; ++i) r[i * kMost + w] = v[i];
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + y), "r"(n * 32) : "memory");
+        }
+        return r;
     }
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N]) {
@@ -481,27 +539,63 @@ struct RowWarps {
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        if (n == 1) return;
-        float* r = red + half * 64;
-        half ^= 1;
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i) r[i * 32 + w] = v[i];
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n * 32) : "memory");
+        if (!CLUSTER && n == 1) return;
+        const float* r = exchange(v);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float4* q = reinterpret_cast<const float4*>(r + i * 32);
+            const float4* q = reinterpret_cast<const float4*>(r + i * kMost);
             float4 t = q[0];
-#pragma unroll
-            for (int k = 1; k * 4 < MOST; ++k) {
-                const float4 a = q[k];
+            auto add = [&](const float4& a) {
                 t.x += a.x;
                 t.y += a.y;
                 t.z += a.z;
                 t.w += a.w;
-            }
+            };
+            if (CLUSTER)
+                for (int k = 1; k * 4 < n; ++k) add(q[k]);
+            else
+#pragma unroll
+                for (int k = 1; k * 4 < kMost; ++k) add(q[k]);
             v[i] = (t.x + t.y) + (t.z + t.w);
         }
+    }
+    __device__ __forceinline__ float warp_total(float2 a) const {
+        float v = a.x + a.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    // From every warp's mean and sum of squares about it, of its EACH columns
+    // (fewer at the row's end): the row's.
+    template <int EACH>
+    __device__ __forceinline__ void merge(float& mean, float& square, int cols, float inv_n) {
+        if (!CLUSTER && n == 1) return;
+        const float v[2] = {mean, square};
+        const float* r = exchange(v);
+        // a lane takes a warp of the row (of a cluster, two), eight lanes all
+        // of a block's eight
+        constexpr int kLanes = CLUSTER ? 32 : kRowWarps, kEach = CLUSTER ? kMost / 32 : 1;
+        auto total = [&](float t) {
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            return t;
+        };
+        float m[kEach], count[kEach], t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = lane % kLanes + i * kLanes;
+            count[i] = (float)max(0, min(EACH, cols - k * EACH));
+            m[i] = r[k];
+            t = fmaf(count[i], m[i], t);
+        }
+        mean = total(t) * inv_n;
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const float d = m[i] - mean;
+            t += fmaf(d * d, count[i], r[kMost + lane % kLanes + i * kLanes]);
+        }
+        square = total(t);
     }
     __device__ __forceinline__ float sum(float2 a) {
         float v[1] = {a.x + a.y};
@@ -539,6 +633,43 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Host: how a row of `cols` columns is shared, V segments a warp: blocks of a
+// cluster, warps a block, and rows a block (of at least `threads` threads).
+struct RowShape {
+    int cluster, warps, rows;
+    template <int V>
+    static RowShape of(int cols, int threads, int most_warps) {
+        const int all = (cols + V * kSeg - 1) / (V * kSeg);
+        RowShape s;
+        s.cluster = 1;
+        while (s.cluster * most_warps < all) s.cluster *= 2;
+        s.warps = (all + s.cluster - 1) / s.cluster;
+        s.rows = s.cluster > 1 || s.warps * 32 >= threads ? 1 : threads / 32 / s.warps;
+        return s;
+    }
+    int threads() const { return 32 * warps * rows; }
+};
+
+// Launches `blocks` clusters of s.cluster blocks.
+template <class Kernel, class Args>
+inline cudaError_t launch_rows(Kernel kernel, const RowShape& s, int64_t blocks, size_t smem,
+                               cudaStream_t stream, const Args& args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(blocks * s.cluster));
+    c.blockDim = dim3((unsigned)s.threads());
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)s.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = s.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, args, s.warps);
 }
 
 // Host: whether a pointer is on a 16-byte boundary (null is).

@@ -185,7 +185,8 @@ def one(rows, cols, dtype, post, pre, gated, per, bias, form, seed=0):
 
 
 @pytest.mark.parametrize("cols", WIDTHS)
-@pytest.mark.parametrize("kind,form,dtype", [(RMS, E4M3, BF16), (LAYER, None, F16), (LAYER, INT8, F32)])
+@pytest.mark.parametrize("kind,form,dtype", [(RMS, E4M3, BF16), (LAYER, None, F16), (LAYER, INT8, F32), (RMS, None, F32),
+                                             (LAYER, None, F32), (LAYER, E4M3, BF16)])
 def test_block_norm_widths(cols, kind, form, dtype):
     rows = 5 if cols > 8192 else 19
     one(rows, cols, dtype, kind, kind, True, 4, kind == LAYER, form, seed=cols)
