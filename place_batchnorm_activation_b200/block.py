@@ -66,29 +66,58 @@ def declare(L) -> None:
 
 
 # ------------------------------------------------------------------ checks
+# A call of a few tokens takes the GPU two to four microseconds, less than an
+# ordinary way of checking ten tensors takes the host.  So what a check needs
+# is looked up once, when torch is there (_Torch), and each check reads every
+# property of a tensor once.
+
+class _Torch:
+    """What the calls need of torch and of the package, looked up at the first
+    call."""
+
+    def __init__(self):
+        import torch
+        from . import IABN_ERR_INVALID_ARG, IabnError, lib
+        self.float32, self.uint8 = torch.float32, torch.uint8
+        self.storage = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        self.formats = {torch.float8_e4m3fn: IABN_Q8_E4M3, torch.int8: IABN_Q8_INT8}
+        self.current_device = torch.cuda.current_device
+        self.current_stream = torch.cuda.current_stream
+        # the current stream of a device without an object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.error, self.invalid = IabnError, IABN_ERR_INVALID_ARG
+        self.lib = lib()
+
+
+_torch = None
+
+
+def _t() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
 
 def _raise(what: str):
     from . import IABN_ERR_INVALID_ARG, IabnError
     raise IabnError(IABN_ERR_INVALID_ARG, what)
 
 
-def _storage(t) -> int:
-    from . import _dtype_code
-    return _dtype_code(t)
-
-
 def _rows_of(t, name: str):
     """(rows, cols, row stride) of a [..., cols] tensor whose rows are evenly
     spaced and whose columns are consecutive."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         _raise(f"{name} has no columns")
-    cols = t.shape[-1]
+    cols = shape[-1]
     if t.is_contiguous():
         return (t.numel() // cols if cols else 0), cols, cols
-    if t.stride(-1) != 1 and cols > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and cols > 1:
         _raise(f"{name}: columns are not consecutive")
     rows, ld = 1, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(shape[-2::-1], strides[-2::-1]):
         if size != 1:
             if ld is None:
                 ld = stride
@@ -102,79 +131,99 @@ class _Call:
     """The tensors of one call, checked: all on the current device, of the
     wanted type and number of elements."""
 
-    __slots__ = ("device", "rows", "cols", "dtype")
+    __slots__ = ("T", "device", "rows", "cols", "numel", "dtype", "storage")
 
     def __init__(self, first, name: str):
-        import torch
-        self.device = first.get_device()
-        if self.device < 0:
+        device = first.get_device()
+        if device < 0:
             _raise(f"{name} is not on a CUDA device")
-        if self.device != torch.cuda.current_device():
-            _raise(f"{name} is on device {self.device}, not on the current one")
+        self.T = T = _t()
+        if device != T.current_device():
+            _raise(f"{name} is on device {device}, not on the current one")
+        self.device = device
         self.rows, self.cols, _ = _rows_of(first, name)
+        self.numel = self.rows * self.cols
         self.dtype = first.dtype
+        self.storage = T.storage.get(first.dtype)
+        if self.storage is None:
+            _raise(f"{name}: unsupported storage dtype {first.dtype}")
 
-    def _ptr(self, t, name: str, dtype, numel: int):
-        if t is None:
-            return None
+    def _refuse(self, t, name: str, dtype, numel: int):
         if t.dtype != dtype:
             _raise(f"{name}: type {t.dtype}, not {dtype}")
         if t.get_device() != self.device:
             _raise(f"{name} is not on the device of the others")
-        if t.numel() != numel or not t.is_contiguous():
-            _raise(f"{name}: {tuple(t.shape)} is not a contiguous tensor of {numel} elements")
-        return t.data_ptr()
+        _raise(f"{name}: {tuple(t.shape)} is not a contiguous tensor of {numel} elements")
 
     def same(self, t, name: str):
         """A contiguous tensor of the first one's type and rows x cols."""
-        if t is not None and t.shape[-1:] != (self.cols,):
+        if t is None:
+            return None
+        if t.dtype != self.dtype or t.get_device() != self.device or t.numel() != self.numel \
+                or not t.is_contiguous():
+            self._refuse(t, name, self.dtype, self.numel)
+        if t.shape[-1] != self.cols:
             _raise(f"{name}: {tuple(t.shape)} has not {self.cols} columns")
-        return self._ptr(t, name, self.dtype, self.rows * self.cols)
+        return t.data_ptr()
+
+    def floats(self, t, name: str, numel: int):
+        """A contiguous float32 tensor of `numel` elements."""
+        if t is None:
+            return None
+        if t.dtype != self.T.float32 or t.get_device() != self.device or t.numel() != numel \
+                or not t.is_contiguous():
+            self._refuse(t, name, self.T.float32, numel)
+        return t.data_ptr()
 
     def strided(self, t, name: str):
         """(pointer, row stride) of a tensor of the first one's type and size."""
         if t.dtype != self.dtype or t.get_device() != self.device:
             _raise(f"{name}: type {t.dtype} on {t.device}, not as the others")
         rows, cols, ld = _rows_of(t, name)
-        if (rows, cols) != (self.rows, self.cols):
+        if rows != self.rows or cols != self.cols:
             _raise(f"{name}: {tuple(t.shape)} is not {self.rows} rows of {self.cols}")
         return t.data_ptr(), ld
 
-    def floats(self, t, name: str, numel: int):
-        import torch
-        return self._ptr(t, name, torch.float32, numel)
-
     def per_col(self, t, name: str):
-        return self.floats(t, name, self.cols)
+        return None if t is None else self.floats(t, name, self.cols)
 
     def per_row(self, t, name: str):
-        return self.floats(t, name, self.rows)
+        return None if t is None else self.floats(t, name, self.rows)
 
     def codes(self, q, scale, name: str, format_of=None):
         """Pointers of codes and scales, and the format."""
-        import torch
         if q is None or scale is None:
             if q is not None or scale is not None:
                 _raise(f"{name}: codes and scales go together")
-            return None, None, None
-        form = {torch.float8_e4m3fn: IABN_Q8_E4M3, torch.int8: IABN_Q8_INT8}.get(q.dtype)
+            return None, None, format_of
+        form = self.T.formats.get(q.dtype)
         if form is None:
             _raise(f"{name}: codes of type {q.dtype}")
-        if format_of not in (None, form):
+        if format_of is not None and format_of != form:
             _raise(f"{name}: codes of two formats in one call")
+        if q.get_device() != self.device or q.numel() != self.numel or not q.is_contiguous():
+            self._refuse(q, name, q.dtype, self.numel)
         groups = -(-self.cols // IABN_Q8_GROUP)
-        return (self._ptr(q, name, q.dtype, self.rows * self.cols),
-                self.floats(scale, f"scale of {name}", self.rows * groups), form)
+        return q.data_ptr(), self.floats(scale, f"scale of {name}", self.rows * groups), form
 
     def gate(self, t, name: str, rows_per_gate: int):
+        if t is None:
+            return None
         if rows_per_gate < 0:
             _raise(f"rows_per_gate = {rows_per_gate}")
         rows = 1 if rows_per_gate == 0 else -(-self.rows // rows_per_gate)
         return self.floats(t, name, rows * self.cols)
 
     def stream(self, stream) -> int:
-        from . import _stream_ptr
-        return _stream_ptr(stream)
+        if stream is None:
+            if self.T.raw_stream is not None:
+                return self.T.raw_stream(self.device)
+            stream = self.T.current_stream()
+        return stream.cuda_stream
+
+    def done(self, status: int, what: str) -> None:
+        if status:
+            raise self.T.error(status, what)
 
 
 def _lib():
@@ -182,16 +231,10 @@ def _lib():
     return lib()
 
 
-def _done(status: int, what: str) -> None:
-    if status:
-        from . import IabnError
-        raise IabnError(status, what)
-
-
 # -------------------------------------------------------------- block norm
 
-def _block(c: _Call, t, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre, form):
-    return IabnBlockDesc(c.rows, c.cols, rows_per_gate, _storage(t), post, pre, form or 0,
+def _block(c: _Call, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre, form):
+    return IabnBlockDesc(c.rows, c.cols, rows_per_gate, c.storage, post, pre, form or 0,
                          residual_scale, eps_post, eps_pre)
 
 
@@ -206,8 +249,8 @@ def block_norm_forward(u, h, h_out, n, *, gamma_post=None, beta_post=None, gate=
     n None (pre = IABN_NORM_NONE): not wanted.  Statistics are written where
     given; u and h_out are what ``block_norm_backward`` takes."""
     c = _Call(h, "h")
-    d = _block(c, h, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre, None)
-    _done(_lib().iabn_block_norm_forward(
+    d = _block(c, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre, None)
+    c.done(c.T.lib.iabn_block_norm_forward(
         ctypes.byref(d), c.same(u, "u"), c.same(h, "h"), c.same(h_out, "h_out"), c.same(n, "n"),
         c.per_col(gamma_post, "gamma_post"), c.per_col(beta_post, "beta_post"),
         c.gate(gate, "gate", rows_per_gate), c.per_col(gamma_pre, "gamma_pre"),
@@ -226,10 +269,9 @@ def block_norm_forward_checkpoint8(u, h, h_out, n, *, q_post=None, scale_post=No
     """``block_norm_forward``, keeping post(u) and pre(h_out) in 8 bits."""
     c = _Call(h, "h")
     qp, sp, form = c.codes(q_post, scale_post, "q_post")
-    qe, se, form_pre = c.codes(q_pre, scale_pre, "q_pre", form)
-    d = _block(c, h, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre,
-               form_pre if form is None else form)
-    _done(_lib().iabn_block_norm_forward_checkpoint8(
+    qe, se, form = c.codes(q_pre, scale_pre, "q_pre", form)
+    d = _block(c, post, pre, rows_per_gate, residual_scale, eps_post, eps_pre, form)
+    c.done(c.T.lib.iabn_block_norm_forward_checkpoint8(
         ctypes.byref(d), c.same(u, "u"), c.same(h, "h"), c.same(h_out, "h_out"), c.same(n, "n"),
         c.per_col(gamma_post, "gamma_post"), c.per_col(beta_post, "beta_post"),
         c.gate(gate, "gate", rows_per_gate), c.per_col(gamma_pre, "gamma_pre"),
@@ -252,8 +294,7 @@ def new_block_norm_workspace(rows: int, cols: int, rows_per_gate: int = 0, devic
 
 
 def _workspace(c: _Call, ws):
-    import torch
-    if ws.get_device() != c.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.get_device() != c.device or ws.dtype != c.T.uint8 or not ws.is_contiguous():
         _raise("workspace: not a contiguous uint8 tensor on the device of the others")
     return ws.data_ptr(), ws.numel()
 
@@ -268,9 +309,9 @@ def block_norm_backward(u, h_out, dh_out, dn, dh, du, workspace, *, mean_post=No
     """Gradients of ``block_norm_forward`` from the kept u and h_out: dh and du
     from dh_out and dn, and those of the parameters that are given."""
     c = _Call(dh, "dh")
-    d = _block(c, dh, post, pre, rows_per_gate, residual_scale, 0.0, 0.0, None)
+    d = _block(c, post, pre, rows_per_gate, residual_scale, 0.0, 0.0, None)
     ws, ws_bytes = _workspace(c, workspace)
-    _done(_lib().iabn_block_norm_backward(
+    c.done(c.T.lib.iabn_block_norm_backward(
         ctypes.byref(d), c.same(u, "u"), c.same(h_out, "h_out"), c.same(dh_out, "dh_out"),
         c.same(dn, "dn"), c.same(dh, "dh"), c.same(du, "du"), c.per_col(gamma_post, "gamma_post"),
         c.per_col(beta_post, "beta_post"), c.gate(gate, "gate", rows_per_gate),
@@ -293,11 +334,10 @@ def block_norm_backward_checkpoint8(q_post, q_pre, dh_out, dn, dh, du, workspace
     """``block_norm_backward`` from the 8-bit checkpoints."""
     c = _Call(dh, "dh")
     qp, sp, form = c.codes(q_post, scale_post, "q_post")
-    qe, se, form_pre = c.codes(q_pre, scale_pre, "q_pre", form)
-    d = _block(c, dh, post, pre, rows_per_gate, residual_scale, 0.0, 0.0,
-               form_pre if form is None else form)
+    qe, se, form = c.codes(q_pre, scale_pre, "q_pre", form)
+    d = _block(c, post, pre, rows_per_gate, residual_scale, 0.0, 0.0, form)
     ws, ws_bytes = _workspace(c, workspace)
-    _done(_lib().iabn_block_norm_backward_checkpoint8(
+    c.done(c.T.lib.iabn_block_norm_backward_checkpoint8(
         ctypes.byref(d), qp, sp, qe, se, c.same(dh_out, "dh_out"), c.same(dn, "dn"),
         c.same(dh, "dh"), c.same(du, "du"), c.per_col(gamma_post, "gamma_post"),
         c.per_col(beta_post, "beta_post"), c.gate(gate, "gate", rows_per_gate),
@@ -322,8 +362,8 @@ def gated_forward(a, b, z, *, act: int = IABN_GLU_SILU, stream=None) -> None:
     """z = phi(a)*b."""
     c = _Call(z, "z")
     pa, pb, ld = _pair(c, a, b, ("a", "b"))
-    d = IabnGatedDesc(c.rows, c.cols, ld, c.cols, _storage(z), act, 0)
-    _done(_lib().iabn_gated_forward(ctypes.byref(d), pa, pb, c.same(z, "z"), c.stream(stream)),
+    d = IabnGatedDesc(c.rows, c.cols, ld, c.cols, c.storage, act, 0)
+    c.done(c.T.lib.iabn_gated_forward(ctypes.byref(d), pa, pb, c.same(z, "z"), c.stream(stream)),
           "iabn_gated_forward")
 
 
@@ -334,8 +374,8 @@ def gated_forward_checkpoint8(a, b, z, qa, scale_a, qb, scale_b, *, act: int = I
     pa, pb, ld = _pair(c, a, b, ("a", "b"))
     ca, sa, form = c.codes(qa, scale_a, "qa")
     cb, sb, form = c.codes(qb, scale_b, "qb", form)
-    d = IabnGatedDesc(c.rows, c.cols, ld, c.cols, _storage(z), act, form or 0)
-    _done(_lib().iabn_gated_forward_checkpoint8(ctypes.byref(d), pa, pb, c.same(z, "z"), ca, sa,
+    d = IabnGatedDesc(c.rows, c.cols, ld, c.cols, c.storage, act, form or 0)
+    c.done(c.T.lib.iabn_gated_forward_checkpoint8(ctypes.byref(d), pa, pb, c.same(z, "z"), ca, sa,
                                                 cb, sb, c.stream(stream)),
           "iabn_gated_forward_checkpoint8")
 
@@ -345,8 +385,8 @@ def gated_backward(a, b, dz, da, db, *, z=None, act: int = IABN_GLU_SILU, stream
     c = _Call(dz, "dz")
     pa, pb, ld = _pair(c, a, b, ("a", "b"))
     pda, pdb, ld_grad = _pair(c, da, db, ("da", "db"))
-    d = IabnGatedDesc(c.rows, c.cols, ld, ld_grad, _storage(dz), act, 0)
-    _done(_lib().iabn_gated_backward(ctypes.byref(d), pa, pb, c.same(dz, "dz"), pda, pdb,
+    d = IabnGatedDesc(c.rows, c.cols, ld, ld_grad, c.storage, act, 0)
+    c.done(c.T.lib.iabn_gated_backward(ctypes.byref(d), pa, pb, c.same(dz, "dz"), pda, pdb,
                                      c.same(z, "z"), c.stream(stream)), "iabn_gated_backward")
 
 
@@ -357,8 +397,8 @@ def gated_backward_checkpoint8(qa, scale_a, qb, scale_b, dz, da, db, *, z=None,
     pda, pdb, ld_grad = _pair(c, da, db, ("da", "db"))
     ca, sa, form = c.codes(qa, scale_a, "qa")
     cb, sb, form = c.codes(qb, scale_b, "qb", form)
-    d = IabnGatedDesc(c.rows, c.cols, c.cols, ld_grad, _storage(dz), act, form or 0)
-    _done(_lib().iabn_gated_backward_checkpoint8(ctypes.byref(d), ca, sa, cb, sb,
+    d = IabnGatedDesc(c.rows, c.cols, c.cols, ld_grad, c.storage, act, form or 0)
+    c.done(c.T.lib.iabn_gated_backward_checkpoint8(ctypes.byref(d), ca, sa, cb, sb,
                                                  c.same(dz, "dz"), pda, pdb, c.same(z, "z"),
                                                  c.stream(stream)),
           "iabn_gated_backward_checkpoint8")
@@ -371,7 +411,7 @@ def checkpoint8_store(x, q, scale, *, stream=None) -> None:
     c = _Call(x, "x")
     px, ld = c.strided(x, "x")
     pq, ps, form = c.codes(q, scale, "q")
-    _done(_lib().iabn_checkpoint8_store(c.rows, c.cols, ld, _storage(x), form or 0, px, pq, ps,
+    c.done(c.T.lib.iabn_checkpoint8_store(c.rows, c.cols, ld, c.storage, form or 0, px, pq, ps,
                                         c.stream(stream)), "iabn_checkpoint8_store")
 
 
@@ -380,6 +420,6 @@ def checkpoint8_load(q, scale, y, *, gamma=None, beta=None, stream=None) -> None
     c = _Call(y, "y")
     py, ld = c.strided(y, "y")
     pq, ps, form = c.codes(q, scale, "q")
-    _done(_lib().iabn_checkpoint8_load(c.rows, c.cols, ld, _storage(y), form or 0, pq, ps,
+    c.done(c.T.lib.iabn_checkpoint8_load(c.rows, c.cols, ld, c.storage, form or 0, pq, ps,
                                        c.per_col(gamma, "gamma"), c.per_col(beta, "beta"), py,
                                        c.stream(stream)), "iabn_checkpoint8_load")

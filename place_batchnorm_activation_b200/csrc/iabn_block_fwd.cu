@@ -244,13 +244,17 @@ constexpr int kStages = 2;
 constexpr int kFwdWarps = 8;      // of a row in one block
 constexpr int kFwdThreads = 256;  // a block's least threads (several rows, if need be)
 
+// Blocks of 256 threads an SM.
+template <int V, bool FULL>
+constexpr int kFwdBlocks = V == 4 ? 1 : FULL ? 2 : 3;
+
 template <int DT, int V, bool FULL>
 size_t shared_bytes(int threads) {
     return ((size_t)kStages * 2 * V * Raw<DT, true>::kQuads + Coef<V, FULL>::kQuads) * 16 * threads;
 }
 
 template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
-__global__ void __launch_bounds__(256, V == 4 ? 1 : FULL ? 2 : 3) block_fwd(const BlockFwd p, int row_warps) {
+__global__ void __launch_bounds__(256, kFwdBlocks<V, FULL>) block_fwd(const BlockFwd p, int row_warps) {
     using T = typename Storage<DT>::T;
     constexpr int Q = Raw<DT, true>::kQuads;
     extern __shared__ uint4 shared[];
@@ -326,14 +330,9 @@ cudaError_t launch_any(const BlockFwd& a, const RowShape& s, cudaStream_t stream
 template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
 cudaError_t launch(const BlockFwd& a, const RowShape& s, cudaStream_t stream, int sms) {
     const size_t smem = shared_bytes<DT, V, FULL>(s.threads());
-    auto kernel = block_fwd<DT, V, FMT, FULL, CLUSTER>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    int blocks = 0;
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, s.threads(), smem);
-    if (e != cudaSuccess) return e;
+    const int blocks = blocks_an_sm(kFwdBlocks<V, FULL>, s.threads(), smem);
     const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * blocks / s.cluster;
-    return launch_rows(kernel, s, need < most ? need : most, smem, stream, a);
+    return launch_rows(block_fwd<DT, V, FMT, FULL, CLUSTER>, s, need < most ? need : most, smem, stream, a);
 }
 
 template <int DT, int V, int FMT>

@@ -652,12 +652,25 @@ struct RowShape {
     int threads() const { return 32 * warps * rows; }
 };
 
+constexpr size_t kFreeShared = 46 * 1024;    // a block's dynamic shared memory without asking
+constexpr size_t kSharedAnSm = 227 * 1024;   // an SM's shared memory for blocks
+
+// Blocks an SM that a kernel with __launch_bounds__(256, `least`) may count on.
+inline int blocks_an_sm(int least, int threads, size_t smem) {
+    const int by_registers = least * 256 / threads;
+    const int by_shared = (int)(kSharedAnSm / (smem + kRedFloats * sizeof(float) + 1024));
+    const int n = by_registers < by_shared ? by_registers : by_shared;
+    return n < 1 ? 1 : n;
+}
+
 // Launches `blocks` clusters of s.cluster blocks.
 template <class Kernel, class Args>
 inline cudaError_t launch_rows(Kernel kernel, const RowShape& s, int64_t blocks, size_t smem,
                                cudaStream_t stream, const Args& args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > kFreeShared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(blocks * s.cluster));
     c.blockDim = dim3((unsigned)s.threads());
