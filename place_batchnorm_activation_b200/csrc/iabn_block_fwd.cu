@@ -112,7 +112,7 @@ struct Params {
 // (In registers they would cost a third of the warps; read for every row, they
 // miss the L1 that is left and double the traffic to L2: 16384 x 4096 layer
 // norms with shifts 188 us.)  FULL: with the shifts.
-template <int V, bool FULL>
+template <bool VEC, int V, bool FULL>
 struct Coef {
     static constexpr int kQuads = (FULL ? 4 : 2) * V * 2;   // a thread's
     float4* mine;   // [which][segment][half] x blockDim
@@ -124,7 +124,7 @@ struct Coef {
             f[2 * i + 1] = make_float2(v.z, v.w);
         }
     }
-    __device__ __forceinline__ void set(int which, const Params<true, V>& from) {
+    __device__ __forceinline__ void set(int which, const Params<VEC, V>& from) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             Lane8 f;
@@ -206,7 +206,7 @@ __device__ __forceinline__ void block_row(const BlockFwd& p, int64_t row, bool h
     }
 }
 
-// Any width and alignment: each row is loaded as its turn comes.
+// Tensors off 16-byte boundaries: each row is loaded as its turn comes.
 constexpr int kAnyV = 2;   // segments a warp
 
 template <int DT, int V, int FMT, bool CLUSTER>
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(256) block_fwd_any(const BlockFwd p, int row_w
     rw.end();
 }
 
-// VEC: a thread copies its share of the rows to come into a
-// ring of its own, kStages - 1 rows ahead.
+// A thread (not VEC: a warp) copies its share of the rows to come into a ring
+// of its own, kStages - 1 rows ahead.
 constexpr int kStages = 2;
 constexpr int kFwdWarps = 8;      // of a row in one block
 constexpr int kFwdThreads = 256;  // a block's least threads (several rows, if need be)
@@ -248,73 +248,99 @@ constexpr int kFwdThreads = 256;  // a block's least threads (several rows, if n
 template <int V, bool FULL>
 constexpr int kFwdBlocks = V == 4 ? 1 : FULL ? 2 : 3;
 
-template <int DT, int V, bool FULL>
+// Bytes of a warp's ring.
+template <int DT, bool VEC, int V>
+constexpr int kFwdRing = kStages * 2 * V * (VEC ? Raw<DT, true>::kQuads * 512
+                                                : kSegBytes<(int)sizeof(typename Storage<DT>::T)>);
+
+template <int DT, bool VEC, int V, bool FULL>
 size_t shared_bytes(int threads) {
-    return ((size_t)kStages * 2 * V * Raw<DT, true>::kQuads + Coef<V, FULL>::kQuads) * 16 * threads;
+    return (size_t)Coef<VEC, V, FULL>::kQuads * 16 * threads + (size_t)kFwdRing<DT, VEC, V> * (threads / 32);
 }
 
-template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
 __global__ void __launch_bounds__(256, kFwdBlocks<V, FULL>) block_fwd(const BlockFwd p, int row_warps) {
     using T = typename Storage<DT>::T;
-    constexpr int Q = Raw<DT, true>::kQuads;
+    constexpr int Q = Raw<DT, true>::kQuads, ES = sizeof(T);
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float red[kRedFloats];
     RowWarps<CLUSTER> rw(row_warps, red);
-    Coef<V, FULL> c{reinterpret_cast<float4*>(shared) + threadIdx.x};
-    uint4* ring = shared + Coef<V, FULL>::kQuads * blockDim.x + threadIdx.x;   // the thread's own
+    Coef<VEC, V, FULL> c{reinterpret_cast<float4*>(shared) + threadIdx.x};
+    uint4* rings = shared + Coef<VEC, V, FULL>::kQuads * blockDim.x;
     const bool has_u = p.u != nullptr;
     const int c0 = rw.w * V * kSeg;
     // a block takes consecutive rows, so that gate rows change seldom
     const int64_t blocks = gridDim.x / (CLUSTER ? cluster_size() : 1);
     const int64_t end = (rw.block + 1) * p.rows / blocks;
     int64_t row = rw.block * p.rows / blocks + rw.y;
-    auto slot = [&](int stage, int tensor, int k, int i) {
-        return ring + (((stage * 2 + tensor) * V + k) * Q + i) * blockDim.x;
+    auto slot = [&](int stage, int tensor, int k, int i) {   // VEC: the thread's
+        return rings + (((stage * 2 + tensor) * V + k) * Q + i) * blockDim.x + threadIdx.x;
+    };
+    auto segment = [&](int stage, int tensor, int k) {       // else the warp's
+        return reinterpret_cast<char*>(rings) + (size_t)(threadIdx.x >> 5) * kFwdRing<DT, VEC, V> +
+               ((stage * 2 + tensor) * V + k) * kSegBytes<ES>;
     };
     auto fetch = [&](int64_t r, int stage) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int col = c0 + k * kSeg + rw.lane * kEl;
-            const bool on = r < end && col < p.cols;
-            const int64_t at = r * p.cols + col;
+            if constexpr (VEC) {
+                const int col = c0 + k * kSeg + rw.lane * kEl;
+                const bool on = r < end && col < p.cols;
+                const int64_t at = r * p.cols + col;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                copy_async<16>(slot(stage, 0, k, i), static_cast<const T*>(p.u) + at + i * 4, on && has_u);
-                copy_async<16>(slot(stage, 1, k, i), static_cast<const T*>(p.h) + at + i * 4, on);
+                for (int i = 0; i < Q; ++i) {
+                    copy_async<16>(slot(stage, 0, k, i), static_cast<const T*>(p.u) + at + i * 4, on && has_u);
+                    copy_async<16>(slot(stage, 1, k, i), static_cast<const T*>(p.h) + at + i * 4, on);
+                }
+            } else {
+                const int left = r < end ? p.cols - c0 - k * kSeg : 0;
+                const int64_t at = r * p.cols + c0 + k * kSeg, total = p.rows * p.cols;
+                copy_segment<ES>(segment(stage, 0, k), p.u, at, has_u ? left : 0, total, rw.lane);
+                copy_segment<ES>(segment(stage, 1, k), p.h, at, left, total, rw.lane);
             }
         }
         copies_end();
     };
     // (what no copy writes, past the row's end and u where there is none, reads as zero)
-    for (int i = 0; i < kStages * 2 * V * Q; ++i) ring[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+    if (VEC)
+        for (int i = 0; i < kStages * 2 * V * Q; ++i) rings[i * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(row + i * rw.rows, i);
-    c.set(kScalePre, Params<true, V>{p, nullptr, c0, rw.lane});
-    if (FULL && p.beta_pre) c.set(kShiftPre, Params<true, V>{p, nullptr, c0, rw.lane});
+    c.set(kScalePre, Params<VEC, V>{p, nullptr, c0, rw.lane});
+    if (FULL && p.beta_pre) c.set(kShiftPre, Params<VEC, V>{p, nullptr, c0, rw.lane});
     int64_t gate_end = -1;   // row at which another gate row begins
     int stage = 0;
     for (; row < end; row += rw.rows) {
         fetch(row + (kStages - 1) * rw.rows, stage == 0 ? kStages - 1 : stage - 1);
         if (row >= gate_end && has_u) {
-            const Params<true, V> from{p, gate_of(p, row), c0, rw.lane};
+            const Params<VEC, V> from{p, gate_of(p, row), c0, rw.lane};
             c.set(kScalePost, from);
             if (FULL && p.beta_post) c.set(kShiftPost, from);
             gate_end = p.gate && p.rows_per_gate > 0 ? (row / p.rows_per_gate + 1) * p.rows_per_gate : end;
         }
         copies_wait<kStages - 1>();
         Lane8 x[V], h[V];
+        if (!VEC) __syncwarp();
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            Raw<DT, true> ru, rh;
+            if constexpr (VEC) {
+                Raw<DT, true> ru, rh;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                ru.v[i] = *slot(stage, 0, k, i);
-                rh.v[i] = *slot(stage, 1, k, i);
+                for (int i = 0; i < Q; ++i) {
+                    ru.v[i] = *slot(stage, 0, k, i);
+                    rh.v[i] = *slot(stage, 1, k, i);
+                }
+                ru.get(x[k]);
+                rh.get(h[k]);
+            } else {
+                const int left = p.cols - c0 - k * kSeg;
+                const int64_t at = row * p.cols + c0 + k * kSeg;
+                read_segment<DT>(segment(stage, 0, k), at, has_u ? left : 0, rw.lane, x[k]);
+                read_segment<DT>(segment(stage, 1, k), at, left, rw.lane, h[k]);
             }
-            ru.get(x[k]);
-            rh.get(h[k]);
         }
-        block_row<DT, true, FULL, V, FMT>(p, row, has_u, c0, c, x, h, rw);
+        if (!VEC) __syncwarp();   // read by all lanes before the next copies into it
+        block_row<DT, VEC, FULL, V, FMT>(p, row, has_u, c0, c, x, h, rw);
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
@@ -327,58 +353,60 @@ cudaError_t launch_any(const BlockFwd& a, const RowShape& s, cudaStream_t stream
     return launch_rows(block_fwd_any<DT, kAnyV, FMT, CLUSTER>, s, need < most ? need : most, 0, stream, a);
 }
 
-template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
 cudaError_t launch(const BlockFwd& a, const RowShape& s, cudaStream_t stream, int sms) {
-    const size_t smem = shared_bytes<DT, V, FULL>(s.threads());
+    const size_t smem = shared_bytes<DT, VEC, V, FULL>(s.threads());
     const int blocks = blocks_an_sm(kFwdBlocks<V, FULL>, s.threads(), smem);
     const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * blocks / s.cluster;
-    return launch_rows(block_fwd<DT, V, FMT, FULL, CLUSTER>, s, need < most ? need : most, smem, stream, a);
+    return launch_rows(block_fwd<DT, VEC, V, FMT, FULL, CLUSTER>, s, need < most ? need : most, smem, stream, a);
 }
 
-template <int DT, int V, int FMT>
+template <int DT, bool VEC, int V, int FMT>
 cudaError_t by_shape(const BlockFwd& a, bool full, cudaStream_t stream, int sms) {
     const RowShape s = RowShape::of<V>(a.cols, kFwdThreads, kFwdWarps);
-    if constexpr (V == 4 || DT == kF32) {
+    if constexpr (V == 4 || DT == kF32 || !VEC) {
         if (s.cluster > 1)
-            return full ? launch<DT, V, FMT, true, true>(a, s, stream, sms)
-                        : launch<DT, V, FMT, false, true>(a, s, stream, sms);
+            return full ? launch<DT, VEC, V, FMT, true, true>(a, s, stream, sms)
+                        : launch<DT, VEC, V, FMT, false, true>(a, s, stream, sms);
     }
-    return full ? launch<DT, V, FMT, true, false>(a, s, stream, sms)
-                : launch<DT, V, FMT, false, false>(a, s, stream, sms);
+    return full ? launch<DT, VEC, V, FMT, true, false>(a, s, stream, sms)
+                : launch<DT, VEC, V, FMT, false, false>(a, s, stream, sms);
 }
 
+// vec: 16-byte accesses; ring: tensors on 16-byte boundaries.
 // Segments a warp, by measurement: two up to 4096 columns (16384 x 4096 bf16,
 // e4m3: 119 us, with four 125), four above, which keep a row of up to 8192 in
 // one block (8192 x 8192: 129 us, 165 with two and a cluster of two blocks).
 // In fp32 four segments and the shifts exceed a block's shared memory: two.
 template <int DT, int FMT>
-cudaError_t by_width(const BlockFwd& a, bool vec, cudaStream_t stream, int sms) {
+cudaError_t by_width(const BlockFwd& a, bool vec, bool ring, cudaStream_t stream, int sms) {
     count_launches(1);
     const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.beta_post || a.beta_pre;
-    if (vec && (a.cols <= 4096 || (DT == kF32 && full))) return by_shape<DT, 2, FMT>(a, full, stream, sms);
-    if (vec) return by_shape<DT, 4, FMT>(a, full, stream, sms);
+    if (vec && (a.cols <= 4096 || (DT == kF32 && full))) return by_shape<DT, true, 2, FMT>(a, full, stream, sms);
+    if (vec) return by_shape<DT, true, 4, FMT>(a, full, stream, sms);
+    if (ring) return by_shape<DT, false, 2, FMT>(a, full, stream, sms);
     const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kFwdWarps);
     return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream, sms)
                          : launch_any<DT, FMT, false>(a, s, stream, sms);
 }
 
 template <int DT>
-cudaError_t by_format(const BlockFwd& a, bool vec, cudaStream_t s, int sms) {
-    if (!a.q_post && !a.q_pre) return by_width<DT, kNoCodes>(a, vec, s, sms);
-    return a.format == kE4M3 ? by_width<DT, kE4M3>(a, vec, s, sms)
-                             : by_width<DT, kInt8>(a, vec, s, sms);
+cudaError_t by_format(const BlockFwd& a, bool vec, bool ring, cudaStream_t s, int sms) {
+    if (!a.q_post && !a.q_pre) return by_width<DT, kNoCodes>(a, vec, ring, s, sms);
+    return a.format == kE4M3 ? by_width<DT, kE4M3>(a, vec, ring, s, sms)
+                             : by_width<DT, kInt8>(a, vec, ring, s, sms);
 }
 
 }  // namespace
 
 cudaError_t block_forward(const BlockFwd& a, int dtype, cudaStream_t s, int sms) {
     if (a.rows == 0) return cudaSuccess;
-    const bool vec = a.cols % kEl == 0 && on16(a.u) && on16(a.h) && on16(a.h_out) && on16(a.n) &&
-                     on16(a.q_post) && on16(a.q_pre);
+    const bool ring = on16(a.u) && on16(a.h);
+    const bool vec = a.cols % kEl == 0 && ring && on16(a.h_out) && on16(a.n) && on16(a.q_post) && on16(a.q_pre);
     switch (dtype) {
-        case kF32: return by_format<kF32>(a, vec, s, sms);
-        case kBF16: return by_format<kBF16>(a, vec, s, sms);
-        default: return by_format<kF16>(a, vec, s, sms);
+        case kF32: return by_format<kF32>(a, vec, ring, s, sms);
+        case kBF16: return by_format<kBF16>(a, vec, ring, s, sms);
+        default: return by_format<kF16>(a, vec, ring, s, sms);
     }
 }
 

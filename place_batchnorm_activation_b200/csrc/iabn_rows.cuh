@@ -635,6 +635,58 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// --------------------------------------------------- a warp's own ring (not VEC)
+// Rows of any width begin on any element, which no asynchronous copy can read.
+// So a warp copies the whole 16-byte words that a segment touches, and its
+// lanes pick their elements from shared memory.  The tensor itself has to
+// begin on a 16-byte boundary, and the last word is cut at its end, so nothing
+// outside of it is read.  (What a word holds of the neighbouring rows is not
+// looked at.)  The warp synchronises between its lanes' copies and reads.
+
+template <int ES>
+constexpr int kSegBytes = kSeg * ES + 16;
+
+// at: the segment's first element; left: columns from there; total: the
+// tensor's elements.
+template <int ES>
+__device__ __forceinline__ void copy_segment(char* dst, const void* base, int64_t at, int left,
+                                             int64_t total, int lane) {
+    const int64_t from = at * ES & ~(int64_t)15;
+    const int words = (int)((at * ES & 15) + min(left, kSeg) * ES + 15) >> 4;
+    const int64_t end = total * ES - from;   // bytes of the tensor from the first word on
+#pragma unroll
+    for (int i = 0; i < (kSegBytes<ES> + 511) / 512; ++i) {
+        const int w = lane + 32 * i;
+        const int bytes = (int)min((int64_t)16, end - w * 16);
+        const bool on = left > 0 && w < words;
+        asm volatile("{ .reg .pred p; setp.ne.b32 p, %3, 0;\n\t"
+                     "@p cp.async.cg.shared.global [%0], [%1], 16, %2; }" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst + w * 16)),
+                     "l"(static_cast<const char*>(base) + from + w * 16), "r"(bytes), "r"((int)on)
+                     : "memory");
+    }
+}
+
+// The lane's eight elements (zero past the row's end).
+template <int DT>
+__device__ __forceinline__ void read_segment(const char* src, int64_t at, int left, int lane, Lane8& f) {
+    using T = typename Storage<DT>::T;
+    const T* p = reinterpret_cast<const T*>(src + (at * (int64_t)sizeof(T) & 15)) + lane;
+#pragma unroll
+    for (int j = 0; j < kEl; ++j) el(f, j) = lane + 32 * j < left ? Storage<DT>::load(p + 32 * j) : 0.f;
+}
+__device__ __forceinline__ Codes<false> read_codes(const char* src, int64_t at, int lane) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(src + (at & 15)) + lane;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __byte_perm(__byte_perm(p[128 * i], p[128 * i + 32], 0x0040),
+                           __byte_perm(p[128 * i + 64], p[128 * i + 96], 0x0040), 0x5410);
+    Codes<false> c;
+    c.v = make_uint2(w[0], w[1]);
+    return c;
+}
+
 // Host: how a row of `cols` columns is shared, V segments a warp: blocks of a
 // cluster, warps a block, and rows a block (of at least `threads` threads).
 struct RowShape {
