@@ -227,7 +227,7 @@ __device__ __forceinline__ void flush_worker(const BlockBwd& p, Lane8 (&C)[V], L
         flush<VEC, V>(E, p.work + (2 * slots + p.workers + rw.block) * W, p.cols, rw, columns);
 }
 
-// Any width and alignment: each row is loaded as its turn comes.
+// Tensors off 16-byte boundaries: each row is loaded as its turn comes.
 constexpr int kAnyV = 2;   // segments a warp
 
 template <int DT, int V, int FMT, bool CLUSTER>
@@ -333,35 +333,37 @@ __global__ void __launch_bounds__(256, 2) block_bwd_any(const BlockBwd p, int ro
     rw.end();
 }
 
-// VEC: a thread copies its share of the rows to come into a
-// ring of its own, two rows ahead, dn and xhat in one group of copies, dh' and
-// uhat in the next: each half of a slot is filled again as soon as the thread
-// has read it.
-// Shared memory of a thread, in 16-byte quads: gate*gamma_post and gamma_pre,
-// and two slots of two halves: a gradient (dn | dh') and what was kept (xhat |
-// uhat).
-template <int DT, int V, int FMT>
+// A thread (not VEC: a warp) copies its share of the rows to come into a ring of
+// its own, two rows ahead, dn and xhat in one group of copies, dh' and uhat in
+// the next: each half of a slot is filled again as soon as it has been read.
+// Shared memory: of a thread, in 16-byte quads, gate*gamma_post and gamma_pre;
+// then two slots of two halves, a gradient (dn | dh') and what was kept (xhat |
+// uhat), in quads of a thread or in bytes of a warp.
+template <int DT, bool VEC, int V, int FMT>
 struct BwdShared {
-    static constexpr int Q = Raw<DT, true>::kQuads;
+    static constexpr int Q = Raw<DT, true>::kQuads, ES = sizeof(typename Storage<DT>::T);
     static constexpr int kCoef = 2 * V * 2;
     static constexpr int kKept = V * Q;   // first quad of what was kept
     static constexpr int kHalf = FMT == kNoCodes ? 2 * V * Q : V * Q + (V + 1) / 2;
-    static constexpr int kQuads = kCoef + 4 * kHalf;
+    static constexpr int kKeptBytes = FMT == kNoCodes ? kSegBytes<ES> : kSegBytes<1>;
+    static constexpr int kHalfBytes = V * (kSegBytes<ES> + kKeptBytes);
+    // of a warp
+    static constexpr int kBytes = kCoef * 512 + 4 * (VEC ? kHalf * 512 : kHalfBytes);
 };
 
 // A row's scalars on one side (pre or post), read into registers a row ahead.
 // (As 4-byte asynchronous copies they cost more than the registers: 167 us in
 // place of 140 for 16384 x 4096 bf16 from e4m3.)
-template <int V>
+template <bool VEC, int V>
 struct Scalars {
-    float rstd, mean, scale[V];
+    float rstd, mean, scale[VEC ? V : 2 * V];
 };
 
-template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
-__global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const BlockBwd p, int row_warps) {
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
+__global__ void __launch_bounds__(256, V == 4 || (FULL && V == 2) ? 1 : 2) block_bwd(const BlockBwd p, int row_warps) {
     using T = typename Storage<DT>::T;
-    using S = BwdShared<DT, V, FMT>;
-    constexpr int Q = S::Q;
+    using S = BwdShared<DT, VEC, V, FMT>;
+    constexpr int Q = S::Q, ES = S::ES;
     constexpr bool CODES = FMT != kNoCodes;
     extern __shared__ float4 shared[];
     __shared__ __align__(16) float red[kRedFloats];
@@ -373,9 +375,19 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
     const int col = c0 + rw.lane * kEl;
     const int group = (c0 >> 7) + (rw.lane >> 4);   // of the lane's first segment
     const bool has_pre = p.pre != kNormNone;
+    // several rows a block: their sums of columns, behind all else
+    float* columns = reinterpret_cast<float*>(reinterpret_cast<char*>(shared) + (blockDim.x >> 5) * S::kBytes);
 
     auto quad = [&](int slot, int half, int i) {
         return mine + (S::kCoef + (slot * 2 + half) * S::kHalf + i) * blockDim.x;
+    };
+    // not VEC: the warp's gradients and kept values of segment k
+    auto segment = [&](int slot, int half, int k) {
+        return reinterpret_cast<char*>(shared + S::kCoef * blockDim.x) +
+               ((threadIdx.x >> 5) * 4 + slot * 2 + half) * S::kHalfBytes + k * kSegBytes<ES>;
+    };
+    auto kept = [&](int slot, int half, int k) {
+        return segment(slot, half, V) + k * S::kKeptBytes;
     };
     // segment k's 8 codes
     auto code = [&](int slot, int half, int k) {
@@ -384,6 +396,18 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
     auto fetch = [&](int slot, int half, int row, bool on) {
         const T* a = static_cast<const T*>(half == 0 ? p.dn : p.dh_out);
         const void* b = half == 0 ? p.sh : p.su;
+        if constexpr (!VEC) {
+            const int64_t total = p.rows * p.cols;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int left = on ? p.cols - c0 - k * kSeg : 0;
+                const int64_t first = (int64_t)row * p.cols + c0 + k * kSeg;
+                copy_segment<ES>(segment(slot, half, k), a, first, a ? left : 0, total, rw.lane);
+                copy_segment<CODES ? 1 : ES>(kept(slot, half, k), b, first, b ? left : 0, total, rw.lane);
+            }
+            copies_end();
+            return;
+        }
         const int64_t at = (int64_t)row * p.cols + col;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -403,43 +427,73 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
         copies_end();
     };
     // what no copy writes (past the row's end, a tensor that is not there) reads as zero
-    for (int i = 0; i < S::kQuads; ++i) mine[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (VEC)
+        for (int i = 0; i < S::kCoef + 4 * S::kHalf; ++i) mine[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
 
-    auto scalars = [&](Scalars<V>& r, bool pre, int row, bool on) {
+    auto scalars = [&](Scalars<VEC, V>& r, bool pre, int row, bool on) {
         const float* rstd = pre ? p.rstd_pre : p.rstd_post;
         r.rstd = on && rstd ? __ldg(rstd + row) : 1.f;
         if constexpr (CODES) {
             const float* scale = pre ? p.scale_pre : p.scale_post;
-            const bool kept = on && (pre ? p.sh : p.su);
+            const bool in = on && (pre ? p.sh : p.su);
+            const float* s = scale + (int64_t)row * p.groups;
+            if constexpr (VEC) {
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                r.scale[k] = kept && col + k * kSeg < p.cols
-                                 ? __ldg(scale + (int64_t)row * p.groups + group + 2 * k) : 0.f;
+                for (int k = 0; k < V; ++k)
+                    r.scale[k] = in && col + k * kSeg < p.cols ? __ldg(s + group + 2 * k) : 0.f;
+            } else {
+                const int g = c0 / kQGroup;
+#pragma unroll
+                for (int k = 0; k < 2 * V; ++k) r.scale[k] = in && g + k < p.groups ? __ldg(s + g + k) : 0.f;
+            }
         } else if constexpr (FULL) {
             const float* mean = pre ? p.mean_pre : p.mean_post;
             r.mean = on && mean ? __ldg(mean + row) : 0.f;
         }
     };
-    auto hat = [&](int slot, int half, int k, const Scalars<V>& r, Lane8& f) {
+    // the normalised values and the gradients of segment k of the row in a slot
+    auto hat = [&](int slot, int half, int k, int row, const Scalars<VEC, V>& r, Lane8& f) {
+        const int left = p.cols - c0 - k * kSeg;
         if constexpr (CODES) {
-            Codes<true> c;
-            c.v = *code(slot, half, k);
-            const float two[2] = {r.scale[k], r.scale[k]};
-            c.template get<FMT>(two, f);
+            if constexpr (VEC) {
+                Codes<true> c;
+                c.v = *code(slot, half, k);
+                const float two[2] = {r.scale[k], r.scale[k]};
+                c.template get<FMT>(two, f);
+            } else {
+                const Codes<false> c = read_codes(kept(slot, half, k), (int64_t)row * p.cols + c0 + k * kSeg, rw.lane);
+                const float two[2] = {r.scale[2 * k], r.scale[2 * k + 1]};
+                c.template get<FMT>(two, f);
+                mask8<false>(f, rw.lane, (half == 0 ? p.sh : p.su) ? left : 0);
+            }
         } else {
-            Raw<DT, true> q;
+            if constexpr (VEC) {
+                Raw<DT, true> q;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, S::kKept + k * Q + i));
-            q.get(f);
+                for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, S::kKept + k * Q + i));
+                q.get(f);
+            } else {
+                read_segment<DT>(kept(slot, half, k), (int64_t)row * p.cols + c0 + k * kSeg,
+                                 (half == 0 ? p.sh : p.su) ? left : 0, rw.lane, f);
+            }
             kept_hat(f, FULL ? r.mean : 0.f, r.rstd);
-            if (FULL) mask8<true>(f, rw.lane, p.cols - c0 - k * kSeg);
+            if (FULL) mask8<VEC>(f, rw.lane, left);
         }
     };
-    auto grad = [&](int slot, int half, int k, Lane8& f) {
-        Raw<DT, true> q;
+    auto grad = [&](int slot, int half, int k, int row, Lane8& f) {
+        if constexpr (VEC) {
+            Raw<DT, true> q;
 #pragma unroll
-        for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, k * Q + i));
-        q.get(f);
+            for (int i = 0; i < Q; ++i) q.v[i] = *reinterpret_cast<uint4*>(quad(slot, half, k * Q + i));
+            q.get(f);
+        } else {
+            read_segment<DT>(segment(slot, half, k), (int64_t)row * p.cols + c0 + k * kSeg,
+                             (half == 0 ? p.dn : p.dh_out) ? p.cols - c0 - k * kSeg : 0, rw.lane, f);
+        }
+    };
+    // not VEC: a warp's copies are there for all of its lanes, or read by all
+    auto lanes_meet = [&]() {
+        if (!VEC) __syncwarp();
     };
     auto coef = [&](int which, int k, Lane8& f) {
 #pragma unroll
@@ -453,7 +507,7 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             Lane8 f;
-            load_weight<true>(gamma, gate, c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, f);
+            load_weight<VEC>(gamma, gate, c0 + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, f);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 mine[((which * V + k) * 2 + i) * blockDim.x] =
@@ -465,7 +519,7 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
     auto fetch_next = [&](int slot, int half) { fetch(slot, half, ahead.at + y, !ahead.done() && ahead.at + y < ahead.hi); };
     fetch_next(0, 0);
     fetch_next(0, 1);
-    Scalars<V> pre, post;
+    Scalars<VEC, V> pre, post;
     scalars(pre, true, st.at + y, st.at + y < st.hi);
     scalars(post, false, st.at + y, st.at + y < st.hi);
     ahead.next();
@@ -481,25 +535,27 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
         zero(E);
     }
     for (int slot = 0; !st.done(); slot ^= 1) {
-        const int64_t row = st.at + y;
+        const int row = st.at + y;
         const bool here = row < st.hi;
         const int next = ahead.at + y;
         const bool next_on = !ahead.done() && next < ahead.hi;
         ahead.next();
         copies_wait<3>();
+        lanes_meet();
         Lane8 g[V], x[V];   // g: dn, then t
         if (has_pre) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                grad(slot, 0, k, g[k]);
-                hat(slot, 0, k, pre, x[k]);
+                grad(slot, 0, k, row, g[k]);
+                hat(slot, 0, k, row, pre, x[k]);
             }
             const float rstd = pre.rstd;
             scalars(pre, true, next, next_on);
+            lanes_meet();
             fetch_next(slot, 0);
             if (here) {
                 const float2 m = pre_half<FULL, V>(g, x, C, E, rw, [&](int k, Lane8& f) { coef(1, k, f); });
-                back_through<true, FULL, V>(g, x, FULL && p.pre == kNormLayer ? m.x * inv_n : 0.f, m.y * inv_n,
+                back_through<VEC, FULL, V>(g, x, FULL && p.pre == kNormLayer ? m.x * inv_n : 0.f, m.y * inv_n,
                                             rstd, p.cols, rw);
             }
         } else {
@@ -507,54 +563,56 @@ __global__ void __launch_bounds__(256, V == 4 || FULL ? 1 : 2) block_bwd(const B
             fetch_next(slot, 0);
         }
         copies_wait<3>();
+        lanes_meet();
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             Lane8 d;
-            grad(slot, 1, k, d);
+            grad(slot, 1, k, row, d);
 #pragma unroll
             for (int j = 0; j < kEl / 2; ++j) g[k][j] = add2(g[k][j], d[j]);
-            hat(slot, 1, k, post, x[k]);
+            hat(slot, 1, k, row, post, x[k]);
         }
         const float rstd = post.rstd;
         scalars(post, false, next, next_on);
+        lanes_meet();
         fetch_next(slot, 1);
         if (here) {
-            const int64_t at = row * p.cols + c0;
+            const int64_t at = (int64_t)row * p.cols + c0;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 Lane8 o;
 #pragma unroll
                 for (int j = 0; j < kEl / 2; ++j) o[j] = mul2(both(p.alpha), g[k][j]);
-                store8<DT, true>(static_cast<T*>(p.dh) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, o);
+                store8<DT, VEC>(static_cast<T*>(p.dh) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, o);
             }
             const float2 m = post_half<FULL, V>(g, x, A, B, rw, p.post != kNormNone,
                                                 [&](int k, Lane8& f) { coef(0, k, f); });
             if (p.post != kNormNone)
-                back_through<true, FULL, V>(g, x, FULL && p.post == kNormLayer ? m.x * inv_n : 0.f,
+                back_through<VEC, FULL, V>(g, x, FULL && p.post == kNormLayer ? m.x * inv_n : 0.f,
                                             m.y * inv_n, rstd, p.cols, rw);
             if (p.du)
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    store8<DT, true>(static_cast<T*>(p.du) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, g[k]);
+                    store8<DT, VEC>(static_cast<T*>(p.du) + at + k * kSeg, rw.lane, p.cols - c0 - k * kSeg, g[k]);
         }
         const bool last = st.last();
-        if (last)   // (behind the ring and the coefficients: the rows' sums of columns)
-            flush_gate<true, FULL, V>(p, st.gate, A, B, rw,
-                                      reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+        if (last)
+            flush_gate<VEC, FULL, V>(p, st.gate, A, B, rw,
+                                      columns);
         st.next();
         if (last && p.gate && p.rows_per_gate > 0 && !st.done())
             set_coef(0, p.gamma_post, p.gate + st.gate * p.cols);
     }
     copies_wait<0>();
-    flush_worker<true, FULL, V>(p, C, E, rw, reinterpret_cast<float*>(shared + S::kQuads * blockDim.x));
+    flush_worker<VEC, FULL, V>(p, C, E, rw, columns);
     rw.end();
 }
 
-// The column pass: a block takes 64 columns, two a thread of a warp, its 16
+// The column pass: a block takes 64 columns, two a thread of a warp, its 32
 // warps share the partial sums of them.  blockIdx.y 0: dgamma_pre, dbeta_pre;
 // 1: dgamma_post, dbeta_post and, of a single gate row, dgate; from 2: the
 // gate rows, of several.
-constexpr int kColWarps = 16;
+constexpr int kColWarps = 32;
 constexpr int kColCols = 64;
 
 // The block's totals of a and b, of column `threadIdx.x` (threads below 64).
@@ -659,21 +717,21 @@ cudaError_t launch_any(const BlockBwd& a, const RowShape& s, cudaStream_t stream
     return launch_rows(block_bwd_any<DT, kAnyV, FMT, CLUSTER>, s, a.workers, columns_bytes(s), stream, a);
 }
 
-template <int DT, int V, int FMT, bool FULL, bool CLUSTER>
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
 cudaError_t launch(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
-    const size_t smem = (size_t)BwdShared<DT, V, FMT>::kQuads * 16 * s.threads() + columns_bytes(s);
-    return launch_rows(block_bwd<DT, V, FMT, FULL, CLUSTER>, s, a.workers, smem, stream, a);
+    const size_t smem = (size_t)BwdShared<DT, VEC, V, FMT>::kBytes * (s.threads() / 32) + columns_bytes(s);
+    return launch_rows(block_bwd<DT, VEC, V, FMT, FULL, CLUSTER>, s, a.workers, smem, stream, a);
 }
 
-template <int DT, int V, int FMT>
+template <int DT, bool VEC, int V, int FMT>
 cudaError_t by_shape(const BlockBwd& a, bool full, cudaStream_t stream) {
     const RowShape s = RowShape::of<V>(a.cols, V == 4 ? kBwdThreads : 2 * kBwdThreads, kBwdWarps);
-    if constexpr (V == 4 || (DT == kF32 && FMT == kNoCodes)) {
+    if constexpr (V == 4 || DT == kF32) {
         if (s.cluster > 1)
-            return full ? launch<DT, V, FMT, true, true>(a, s, stream)
-                        : launch<DT, V, FMT, false, true>(a, s, stream);
+            return full ? launch<DT, VEC, V, FMT, true, true>(a, s, stream)
+                        : launch<DT, VEC, V, FMT, false, true>(a, s, stream);
     }
-    return full ? launch<DT, V, FMT, true, false>(a, s, stream) : launch<DT, V, FMT, false, false>(a, s, stream);
+    return full ? launch<DT, VEC, V, FMT, true, false>(a, s, stream) : launch<DT, VEC, V, FMT, false, false>(a, s, stream);
 }
 
 // Segments a warp, by measurement (bf16 from e4m3): with all four sums of
@@ -682,25 +740,37 @@ cudaError_t by_shape(const BlockBwd& a, bool full, cudaStream_t stream) {
 // and 92); with two sums both fit, and two segments are as fast up to 4096
 // columns (16384 x 4096: 130 and 132 us; x 1024: 41 and 44), while above four
 // keep a row in one block (8192 x 8192: 196 us with a cluster of two, 143).
+// One segment a warp makes a row's way through its warps shorter, which counts
+// where a worker has few rows: 3001 x 1021 kept fp32 53 us with two, 32 with
+// one; 300 x 2048 16.7 and 12.6; and up to 1024 columns with all four sums
+// always (16384 x 1024: 59 and 52).
+// In fp32 four take too much shared memory for more than one small block an SM:
+// two (3001 x 4096 kept: 131 and 111 us), and clusters above 4096 columns.
+template <int DT, bool VEC, int FMT>
+cudaError_t by_width(const BlockBwd& a, bool full, cudaStream_t stream) {
+    if (a.cols <= 2048 && ((full && a.cols <= 1024) || a.rows < 16 * a.workers))
+        return by_shape<DT, VEC, 1, FMT>(a, full, stream);
+    if constexpr (DT != kF32)
+        if (a.cols > (full ? 1024 : 4096)) return by_shape<DT, VEC, 4, FMT>(a, full, stream);
+    return by_shape<DT, VEC, 2, FMT>(a, full, stream);
+}
+
+// vec: 16-byte accesses; ring: tensors on 16-byte boundaries.
 template <int DT, int FMT>
-cudaError_t by_width(const BlockBwd& a, bool vec, cudaStream_t stream) {
+cudaError_t by_alignment(const BlockBwd& a, bool vec, bool ring, cudaStream_t stream) {
     count_launches(1);
     const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.dbeta_post || a.dbeta_pre ||
                       (a.dgate && a.beta_post);
-    if (!vec) {
-        const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kBwdWarps);
-        return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream) : launch_any<DT, FMT, false>(a, s, stream);
-    }
-    // (kept fp32 tensors of wider rows exceed a block's shared memory with four)
-    constexpr bool kWide = DT == kF32 && FMT == kNoCodes;
-    if (a.cols > (full ? 2 * kSeg : 4096) && !(kWide && a.cols > 4096)) return by_shape<DT, 4, FMT>(a, full, stream);
-    return by_shape<DT, 2, FMT>(a, full, stream);
+    if (vec) return by_width<DT, true, FMT>(a, full, stream);
+    if (ring) return by_width<DT, false, FMT>(a, full, stream);
+    const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kBwdWarps);
+    return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream) : launch_any<DT, FMT, false>(a, s, stream);
 }
 
 template <int DT>
-cudaError_t by_format(const BlockBwd& a, bool vec, bool codes, cudaStream_t s) {
-    if (!codes) return by_width<DT, kNoCodes>(a, vec, s);
-    return a.format == kE4M3 ? by_width<DT, kE4M3>(a, vec, s) : by_width<DT, kInt8>(a, vec, s);
+cudaError_t by_format(const BlockBwd& a, bool vec, bool ring, bool codes, cudaStream_t s) {
+    if (!codes) return by_alignment<DT, kNoCodes>(a, vec, ring, s);
+    return a.format == kE4M3 ? by_alignment<DT, kE4M3>(a, vec, ring, s) : by_alignment<DT, kInt8>(a, vec, ring, s);
 }
 
 }  // namespace
@@ -714,11 +784,11 @@ int64_t block_bwd_workers(int64_t rows, int64_t cols) {
 
 cudaError_t block_backward(const BlockBwd& a, int dtype, bool codes, cudaStream_t s, int) {
     if (a.rows > 0) {
-        const bool vec = a.cols % kEl == 0 && on16(a.su) && on16(a.sh) && on16(a.dh_out) &&
-                         on16(a.dn) && on16(a.dh) && on16(a.du);
-        const cudaError_t e = dtype == kF32    ? by_format<kF32>(a, vec, codes, s)
-                              : dtype == kBF16 ? by_format<kBF16>(a, vec, codes, s)
-                                               : by_format<kF16>(a, vec, codes, s);
+        const bool ring = on16(a.su) && on16(a.sh) && on16(a.dh_out) && on16(a.dn);
+        const bool vec = a.cols % kEl == 0 && ring && on16(a.dh) && on16(a.du);
+        const cudaError_t e = dtype == kF32    ? by_format<kF32>(a, vec, ring, codes, s)
+                              : dtype == kBF16 ? by_format<kBF16>(a, vec, ring, codes, s)
+                                               : by_format<kF16>(a, vec, ring, codes, s);
         if (e != cudaSuccess) return e;
     }
     const bool pre = a.dgamma_pre || a.dbeta_pre, post = a.dgamma_post || a.dbeta_post;

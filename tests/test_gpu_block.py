@@ -162,16 +162,26 @@ WIDTHS = [1, 2, 7, 8, 64, 127, 128, 129, 200, 256, 257, 512, 1000, 1021, 1024, 2
           8193, 12000, 16384, 20001, 32768]
 
 
-def one(rows, cols, dtype, post, pre, gated, per, bias, form, seed=0):
+def off_boundary(t):
+    """The same values one element behind a 16-byte boundary."""
+    if t is None:
+        return None
+    flat = torch.empty(t.numel() + 16, dtype=t.dtype, device=t.device)
+    out = flat[1:1 + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def one(rows, cols, dtype, post, pre, gated, per, bias, form, seed=0, place=lambda t: t):
     """Forward, then the backward from what it kept, both against 64 bits."""
     what = f"{rows}x{cols} {dtype} post {post} pre {pre} gate {gated}/{per} {form}"
     o = params(rows, cols, post, pre, gated, per, bias, seed + 3)
-    u = values(rows, cols, dtype, seed, 1.0, 0.3)
-    h = values(rows, cols, dtype, seed + 1, 2.0, 0.5)
+    u = place(values(rows, cols, dtype, seed, 1.0, 0.3))
+    h = place(values(rows, cols, dtype, seed + 1, 2.0, 0.5))
     got = run_forward(u, h, o, form)
     check_forward(u, h, o, form, got, what)
-    dh_out = values(rows, cols, dtype, seed + 5, 0.1)
-    dn = values(rows, cols, dtype, seed + 6, 0.1) if pre else None
+    dh_out = place(values(rows, cols, dtype, seed + 5, 0.1))
+    dn = place(values(rows, cols, dtype, seed + 6, 0.1)) if pre else None
     stats = {k: got.get(k) for k in ("mean_post", "rstd_post", "mean_pre", "rstd_pre") if got.get(k) is not None}
     if form is None:
         src_u, src_x = u, got["h_out"] if pre else None
@@ -202,9 +212,16 @@ def test_block_norm_forms(dtype, post, pre, gated, per, bias, form):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 7, 147, 149, 296, 297, 1201])
-@pytest.mark.parametrize("cols,per", [(72, 0), (72, 5), (520, 300), (1032, 2), (4096, 64)])
+@pytest.mark.parametrize("cols,per", [(72, 0), (72, 5), (73, 4), (520, 300), (1032, 2), (1021, 100), (4096, 64)])
 def test_block_norm_rows(rows, cols, per):
     one(rows, cols, BF16, RMS, RMS, True, per, False, E4M3, seed=rows)
+
+
+@pytest.mark.parametrize("dtype,form", [(BF16, E4M3), (F16, None), (F32, INT8), (F32, None)])
+@pytest.mark.parametrize("cols", [1, 9, 256, 1000, 4096, 4099, 9000, 32768])
+def test_block_norm_off_16_byte_boundaries(cols, dtype, form):
+    one(7, cols, dtype, LAYER, LAYER, True, 3, True, form, seed=cols, place=off_boundary)
+    one(7, cols, dtype, RMS, RMS, False, 0, False, form, seed=cols, place=off_boundary)
 
 
 @pytest.mark.parametrize("form", [None, E4M3])
