@@ -5,10 +5,17 @@
 //   uhat = post(u);  h' = alpha h + gate (gamma_post uhat + beta_post);
 //   xhat = pre(h');  n = gamma_pre xhat + beta_pre.
 //
-// A row is held in registers between its two reductions, eight columns a lane
-// and segment.
-// Bound: HBM bandwidth, 4 s bytes an element (s the storage size), 2 more
-// with checkpoints.
+// A row is held in registers between its two reductions (one for each norm),
+// eight columns a lane and segment; the rows to come are on their way into
+// shared memory meanwhile.  What a lane does by itself is what bounds it before
+// HBM does, so values are worked on two at a time and a division serves four
+// checkpoint groups.
+// Floor: 4 s bytes an element (s the storage size), 2 more with checkpoints.
+// Measured (GPU time, B200): 16384 x 4096 bf16, RMS norms, e4m3 checkpoints
+// 121 us (5.6 TB/s, floor 105 at the 6.43 TB/s of a copy); layer norms with
+// shifts 162 us; 8192 x 8192 128 us; 3001 x 1021 fp16 layer norms 14.1 us
+// (floor 3.8); 8 x 4096 without checkpoints 3.6 us, the launch's own time and
+// two reductions.
 #include "iabn_rows.cuh"
 
 namespace iabn {

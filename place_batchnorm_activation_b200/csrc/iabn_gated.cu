@@ -5,8 +5,14 @@
 // 2 sqrt(2/pi) (a + 0.044715 a^3) (GELU_TANH: (1 + tanh y)/2 = 1/(1 + e^-2y),
 // which does not cancel for large negative y), or the normal distribution
 // function (GELU), so phi' = w + a w'.
-// Elementwise; a warp takes 256 columns (two checkpoint groups) of many rows.  Bound: HBM bandwidth: 3 s bytes an element forward (2 more with
-// checkpoints), 3 s + 2 backward from codes, s more for z.
+// Elementwise; a warp takes 256 columns (two checkpoint groups) of many rows.
+// Floor: 3 s bytes an element forward (2 more with checkpoints), 3 s + 2
+// backward from codes, s more for z.
+// Measured (GPU time, B200): 8192 x 14336 bf16 SiLU with int8 checkpoints,
+// forward 162 us (5.8 TB/s, floor 147), backward with z 194 us (floor 184);
+// storing 16384 x 5120 bf16 as e4m3 45 us (floor 39.5), loading 16384 x 4096
+// with a scale 36 us (floor 31.6); 777 x 2731 fp16 GELU backward 12 us (floor
+// 2.7: elements one by one, and erfc).
 #include "iabn_rows.cuh"
 
 namespace iabn {
