@@ -224,6 +224,46 @@ def test_block_norm_off_16_byte_boundaries(cols, dtype, form):
     one(7, cols, dtype, RMS, RMS, False, 0, False, form, seed=cols, place=off_boundary)
 
 
+@pytest.mark.parametrize("cols", [40, 41, 1024, 9000, 9001])
+@pytest.mark.parametrize("post,pre", [(RMS, LAYER), (NONE, NONE), (NONE, RMS)])
+def test_block_norm_gate_of_more_rows_than_there_are(cols, post, pre):
+    """One gate row that covers more rows than the call has; widths that share
+    rows in clusters, with and without a norm to wait for."""
+    one(6, cols, BF16, post, pre, True, 1 << 40, True, INT8, seed=cols)
+    one(6, cols, F32, post, pre, True, 7, True, None, seed=cols)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, give what they
+    give one after the other."""
+    rows, cols = 900, 2056
+    o = params(rows, cols, RMS, LAYER, True, 300, True, 1)
+    sets = []
+    for k in range(2):
+        u, h = values(rows, cols, BF16, 10 * k), values(rows, cols, BF16, 10 * k + 1)
+        f = run_forward(u, h, o, E4M3)
+        g = [values(rows, cols, BF16, 10 * k + 2), values(rows, cols, BF16, 10 * k + 3)]
+        src = ((f["q_post"], f["scale_post"]), (f["q_pre"], f["scale_pre"]))
+        stats = {"rstd_post": f["rstd_post"], "rstd_pre": f["rstd_pre"]}
+        sets.append((src, g, stats, run_backward(*src, *g, o, stats), torch.cuda.Stream()))
+    keys = ("post", "pre", "rows_per_gate", "residual_scale", "gamma_post", "beta_post", "gate", "gamma_pre")
+    outs = []
+    for _, g, _, want, _ in sets:
+        t = {k: torch.empty_like(v) for k, v in want.items()}
+        outs.append((t, iabn.new_block_norm_workspace(rows, cols, 300, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (src, g, stats, want, stream), (t, ws) in zip(sets, outs):
+            (qu, su), (qx, sx) = src
+            grads = {k: v for k, v in t.items() if k not in ("dh", "du")}
+            iabn.block_norm_backward_checkpoint8(qu, qx, g[0], g[1], t["dh"], t["du"], ws, scale_post=su, scale_pre=sx,
+                                                 **stats, **grads, **{k: o[k] for k in keys}, stream=stream)
+    torch.cuda.synchronize()
+    for (_, _, _, want, _), (t, _) in zip(sets, outs):
+        for k in want:
+            assert torch.equal(want[k], t[k]), k
+
+
 @pytest.mark.parametrize("form", [None, E4M3])
 def test_block_norm_without_u_and_partial_gradients(form):
     """The norm of h alone; gradients that are not wanted are left out."""
