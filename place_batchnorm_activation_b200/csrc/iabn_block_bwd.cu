@@ -724,13 +724,13 @@ size_t columns_bytes(const RowShape& s) {
 
 template <int DT, int FMT, bool CLUSTER>
 cudaError_t launch_any(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
-    return launch_rows(block_bwd_any<DT, kAnyV, FMT, CLUSTER>, s, a.workers, columns_bytes(s), stream, a);
+    return launch_rows<block_bwd_any<DT, kAnyV, FMT, CLUSTER>>(s, a.workers, columns_bytes(s), stream, a);
 }
 
 template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
 cudaError_t launch(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
     const size_t smem = (size_t)BwdShared<DT, VEC, V, FMT>::kBytes * (s.threads() / 32) + columns_bytes(s);
-    return launch_rows(block_bwd<DT, VEC, V, FMT, FULL, CLUSTER>, s, a.workers, smem, stream, a);
+    return launch_rows<block_bwd<DT, VEC, V, FMT, FULL, CLUSTER>>(s, a.workers, smem, stream, a);
 }
 
 template <int DT, bool VEC, int V, int FMT>

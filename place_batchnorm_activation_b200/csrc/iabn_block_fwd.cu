@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(256, kFwdBlocks<V, FULL>) block_fwd(const Bloc
 template <int DT, int FMT, bool CLUSTER>
 cudaError_t launch_any(const BlockFwd& a, const RowShape& s, cudaStream_t stream, int sms) {
     const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * 32 / s.cluster;
-    return launch_rows(block_fwd_any<DT, kAnyV, FMT, CLUSTER>, s, need < most ? need : most, 0, stream, a);
+    return launch_rows<block_fwd_any<DT, kAnyV, FMT, CLUSTER>>(s, need < most ? need : most, 0, stream, a);
 }
 
 template <int DT, bool VEC, int V, int FMT, bool FULL, bool CLUSTER>
@@ -365,7 +365,7 @@ cudaError_t launch(const BlockFwd& a, const RowShape& s, cudaStream_t stream, in
     const size_t smem = shared_bytes<DT, VEC, V, FULL>(s.threads());
     const int blocks = blocks_an_sm(kFwdBlocks<V, FULL>, s.threads(), smem);
     const int64_t need = (a.rows + s.rows - 1) / s.rows, most = (int64_t)sms * blocks / s.cluster;
-    return launch_rows(block_fwd<DT, VEC, V, FMT, FULL, CLUSTER>, s, need < most ? need : most, smem, stream, a);
+    return launch_rows<block_fwd<DT, VEC, V, FMT, FULL, CLUSTER>>(s, need < most ? need : most, smem, stream, a);
 }
 
 template <int DT, bool VEC, int V, int FMT>

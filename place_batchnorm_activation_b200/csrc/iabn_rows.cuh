@@ -19,6 +19,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "iabn_block_internal.h"
 #include "iabn_device.cuh"
 
@@ -715,13 +717,27 @@ inline int blocks_an_sm(int least, int threads, size_t smem) {
     return n < 1 ? 1 : n;
 }
 
-// Launches `blocks` clusters of s.cluster blocks.
-template <class Kernel, class Args>
-inline cudaError_t launch_rows(Kernel kernel, const RowShape& s, int64_t blocks, size_t smem,
-                               cudaStream_t stream, const Args& args) {
+// Launches `blocks` clusters of s.cluster blocks.  A kernel serves many widths
+// with as many amounts of shared memory, from several host threads: its limit
+// is raised once on each device, to all that a block may have, and never
+// lowered (a call that set its own amount could fail another thread's launch).
+template <auto KERNEL, class Args>
+inline cudaError_t launch_rows(const RowShape& s, int64_t blocks, size_t smem, cudaStream_t stream,
+                               const Args& args) {
     if (smem > kFreeShared) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> raised{0};   // a bit a device
+        int dev = 0, most = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (!(raised.load(std::memory_order_acquire) & bit)) {
+            e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     most - (int)(kRedFloats * sizeof(float)));
+            if (e != cudaSuccess) return e;
+            raised.fetch_or(bit, std::memory_order_release);
+        }
     }
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(blocks * s.cluster));
@@ -734,7 +750,7 @@ inline cudaError_t launch_rows(Kernel kernel, const RowShape& s, int64_t blocks,
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = s.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&c, kernel, args, s.warps);
+    return cudaLaunchKernelEx(&c, KERNEL, args, s.warps);
 }
 
 // Host: whether a pointer is on a 16-byte boundary (null is).
