@@ -23,7 +23,10 @@
  *     are written as zeros.
  *   - An output in the storage type may be the same tensor as an input in it
  *     (same start, same row stride), which it then overwrites; any other
- *     overlap of an output with an input or output is IABN_ERR_INVALID_ARG.
+ *     overlap of an output (codes, scales, statistics, parameter gradients and
+ *     the workspace's needed bytes included) with an input or output is
+ *     IABN_ERR_INVALID_ARG.  Tensors of different row strides count as
+ *     overlapping where their ranges meet.
  *   - Calls keep no state: a workspace needs no clearing and may serve any
  *     calls that do not run at the same time.  All can be captured into a
  *     CUDA graph.

@@ -83,24 +83,35 @@ bool disjoint(const Region& a, const Region& b) {
     return d >= (uintptr_t)a.width && d + (uintptr_t)b.width <= L;
 }
 
-// Outputs among themselves disjoint; an output and an input disjoint, or the
-// same tensor where the input is `inplace` (in the storage type).
+Region floats(const void* p, int64_t rows, int64_t cols) { return region(p, rows, cols, cols, 4); }
+
+// A call's tensors.  Outputs are disjoint from each other and from the inputs,
+// but for an output in the storage type, which may be an input in it.
 struct Overlaps {
-    Region in[8], out[8], fixed[8];
-    int ni = 0, no = 0, nf = 0;
-    void input(const Region& r) { in[ni++] = r; }
-    void output(const Region& r) { out[no++] = r; }
-    void read_only(const Region& r) { fixed[nf++] = r; }
+    struct Tensor {
+        Region at;
+        bool storage;
+    } in[16], out[16];
+    int ni = 0, no = 0;
+    void input(const Region& r) { add(in, ni, r, true); }
+    void output(const Region& r) { add(out, no, r, true); }
+    void other_input(const Region& r) { add(in, ni, r, false); }     // codes, scales, parameters, statistics
+    void other_output(const Region& r) { add(out, no, r, false); }   // these, gradients of parameters, workspace
     bool ok() const {
         for (int i = 0; i < no; ++i) {
             for (int j = 0; j < i; ++j)
-                if (!disjoint(out[i], out[j])) return false;
+                if (!disjoint(out[i].at, out[j].at)) return false;
             for (int j = 0; j < ni; ++j)
-                if (!disjoint(out[i], in[j]) && !same(out[i], in[j])) return false;
-            for (int j = 0; j < nf; ++j)
-                if (!disjoint(out[i], fixed[j])) return false;
+                if (!disjoint(out[i].at, in[j].at) &&
+                    !(out[i].storage && in[j].storage && same(out[i].at, in[j].at)))
+                    return false;
         }
         return true;
+    }
+
+private:
+    static void add(Tensor* list, int& n, const Region& r, bool storage) {
+        if (r.at && r.rows > 0) list[n++] = {r, storage};
     }
 };
 
@@ -162,8 +173,12 @@ iabn_status block_fwd_call(const iabn_block_desc* d, const void* u, const void* 
     o.input(whole(d, h));
     o.output(whole(d, h_out));
     o.output(whole(d, n));
-    o.output(bytes(d, q_post));
-    o.output(bytes(d, q_pre));
+    o.other_output(bytes(d, q_post));
+    o.other_output(bytes(d, q_pre));
+    for (const float* p : {scale_post, scale_pre}) o.other_output(floats(p, d->rows, q_groups(d->cols)));
+    for (const float* p : {mean_post, rstd_post, mean_pre, rstd_pre}) o.other_output(floats(p, d->rows, 1));
+    for (const float* p : {gamma_post, beta_post, gamma_pre, beta_pre}) o.other_input(floats(p, 1, d->cols));
+    o.other_input(floats(gate, gate_rows(d), d->cols));
     if (!o.ok()) return IABN_ERR_INVALID_ARG;
     int sms = 0;
     const cudaError_t e = current_sms(sms);
@@ -243,16 +258,25 @@ iabn_status block_bwd_call(const iabn_block_desc* d, bool codes, const void* su,
     o.input(whole(d, dh_out));
     o.input(whole(d, dn));
     if (codes) {
-        o.read_only(bytes(d, su));
-        o.read_only(bytes(d, sh));
+        o.other_input(bytes(d, su));
+        o.other_input(bytes(d, sh));
+        if (su) o.other_input(floats(scale_post, d->rows, q_groups(d->cols)));
+        if (sh) o.other_input(floats(scale_pre, d->rows, q_groups(d->cols)));
     } else {
         o.input(whole(d, su));
         o.input(whole(d, sh));
     }
+    for (const float* p : {gamma_post, beta_post, gamma_pre}) o.other_input(floats(p, 1, d->cols));
+    o.other_input(floats(gate, gate_rows(d), d->cols));
+    for (const float* p : {mean_post, rstd_post, mean_pre, rstd_pre}) o.other_input(floats(p, d->rows, 1));
     o.output(whole(d, dh));
     o.output(whole(d, du));
+    for (const float* p : {dgamma_post, dbeta_post, dgamma_pre, dbeta_pre}) o.other_output(floats(p, 1, d->cols));
+    o.other_output(floats(dgate, gate_rows(d), d->cols));
+    const size_t need = block_ws_bytes(d);
+    o.other_output(region(workspace, 1, (int64_t)need, (int64_t)need, 1));
     if (!o.ok()) return IABN_ERR_INVALID_ARG;
-    if (!workspace || ws_bytes < block_ws_bytes(d) || misaligned(16, {workspace}))
+    if (!workspace || ws_bytes < need || misaligned(16, {workspace}))
         return IABN_ERR_WORKSPACE;
     int sms = 0;
     const cudaError_t e = current_sms(sms);
@@ -315,8 +339,8 @@ iabn_status gated_fwd_call(const iabn_gated_desc* d, const void* a, const void* 
     o.input(region(a, d->rows, d->cols, d->ld, es));
     o.input(region(b, d->rows, d->cols, d->ld, es));
     o.output(region(z, d->rows, d->cols, d->cols, es));
-    o.output(region(qa, d->rows, d->cols, d->cols, 1));
-    o.output(region(qb, d->rows, d->cols, d->cols, 1));
+    for (const void* q : {qa, qb}) o.other_output(region(q, d->rows, d->cols, d->cols, 1));
+    for (const float* p : {sa, sb}) o.other_output(floats(p, d->rows, q_groups(d->cols)));
     if (!o.ok()) return IABN_ERR_INVALID_ARG;
     int sms = 0;
     const cudaError_t e = current_sms(sms);
@@ -351,8 +375,8 @@ iabn_status gated_bwd_call(const iabn_gated_desc* d, bool codes, const void* a, 
     Overlaps o;
     o.input(region(dz, d->rows, d->cols, d->cols, es));
     if (codes) {
-        o.read_only(region(a, d->rows, d->cols, d->cols, 1));
-        o.read_only(region(b, d->rows, d->cols, d->cols, 1));
+        for (const void* q : {a, b}) o.other_input(region(q, d->rows, d->cols, d->cols, 1));
+        for (const float* p : {sa, sb}) o.other_input(floats(p, d->rows, q_groups(d->cols)));
     } else {
         o.input(region(a, d->rows, d->cols, d->ld, es));
         o.input(region(b, d->rows, d->cols, d->ld, es));
@@ -398,8 +422,18 @@ iabn_status check8_call(bool load, int64_t rows, int64_t cols, int64_t ld, int32
     if (!t || !q || !scale) return IABN_ERR_INVALID_ARG;
     const int es = elem_size(dtype);
     if (misaligned(es, {t}) || misaligned(4, {scale, gamma, beta})) return IABN_ERR_MISALIGNED;
-    if (!disjoint(region(t, rows, cols, ld, es), region(q, rows, cols, cols, 1)))
-        return IABN_ERR_INVALID_ARG;
+    Overlaps o;
+    if (load) {
+        o.output(region(y, rows, cols, ld, es));
+        o.other_input(region(q, rows, cols, cols, 1));
+        o.other_input(floats(scale, rows, q_groups(cols)));
+        for (const float* p : {gamma, beta}) o.other_input(floats(p, 1, cols));
+    } else {
+        o.input(region(x, rows, cols, ld, es));
+        o.other_output(region(q, rows, cols, cols, 1));
+        o.other_output(floats(scale, rows, q_groups(cols)));
+    }
+    if (!o.ok()) return IABN_ERR_INVALID_ARG;
     int sms = 0;
     const cudaError_t e = current_sms(sms);
     if (e != cudaSuccess) return from_cuda(e);
