@@ -594,7 +594,8 @@ struct RowWarps {
         t = 0.f;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const float d = m[i] - mean;
+            // (a warp without columns adds nothing, even where mean^2 overflows)
+            const float d = count[i] > 0.f ? m[i] - mean : 0.f;
             t += fmaf(d * d, count[i], r[kMost + lane % kLanes + i * kLanes]);
         }
         square = total(t);

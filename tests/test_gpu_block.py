@@ -797,3 +797,38 @@ def test_a_feed_forward_block_and_its_gradients(form):
     near(dw1, DP.t() @ (X0 * D(g0)), "dw1")
     near(dg0, (DN0 * X0).sum(0), "dgamma_0")
     near(dh0, T + back(DN0 * D(g0), X0, rho[0]), "dh0")
+
+
+@pytest.mark.parametrize("dtype,value", [(BF16, 1e20), (F32, 1e20), (F32, 1e22), (F16, 6e4)])
+@pytest.mark.parametrize("cols", [256, 512, 600, 1024, 1536, 2056, 3000, 4096, 5120, 8192, 8200, 9001, 20001, 32768])
+def test_constant_rows_of_large_values(cols, dtype, value):
+    """A layer norm of rows whose every value is the same: the variance is 0 (but
+    for what the mean's rounding leaves of the value), whatever part of the
+    row's warps has columns, and nothing is NaN.
+
+    A row's sum is exact, as count * value takes fewer than 24 bits of a value of
+    8 bits (bf16; the fp32 values are rounded to bf16).  Its product with 1/cols is
+    off by at most 2^-23 of the mean, so where cols is a power of two nothing is
+    lost; elsewhere the deviation d <= 2^-22 |mean| from the mean gives a variance
+    of at most d^2."""
+    u = torch.full((3, cols), value, dtype=dtype, device="cuda").to(BF16).to(dtype)
+    u[1] = -u[1]
+    u[2] = torch.randn(cols, generator=gen(1)).to(dtype).cuda()
+    h = torch.zeros_like(u)
+    for form in (None, E4M3):
+        o = params(3, cols, LAYER, LAYER, False, 0, False, 1) | {"gamma_post": None, "gamma_pre": None}
+        got = run_forward(u, h, o, form)
+        assert not any(torch.isnan(t.float()).any() for t in got.values() if t is not None)
+        if form is None:
+            mean = u[:2, 0].float()
+            assert ((got["mean_post"][:2] - mean).abs() <= 2.0 ** -22 * mean.abs()).all()
+            least = 1.0 / (EPS["eps_post"] + (2.0 ** -22 * mean.double()) ** 2).sqrt()
+            assert (got["rstd_post"][:2].double() >= least * (1 - 1e-5)).all()
+            assert (got["rstd_post"][:2].double() <= EPS["eps_post"] ** -0.5 * (1 + 1e-5)).all()
+        if cols & (cols - 1) == 0:
+            assert (got["h_out"][:2] == 0).all() and (got["n"][:2] == 0).all()
+    # the ordinary row beside them
+    w = u[2:].double()
+    want = (w - w.mean()) * ((w - w.mean()).square().mean() + EPS["eps_post"]) ** -0.5
+    step = torch.finfo(dtype).eps
+    assert ((got["h_out"][2:].double() - want).abs() <= (step + 1e-5) * (1 + want.abs())).all()
