@@ -733,15 +733,13 @@ cudaError_t launch(const BlockBwd& a, const RowShape& s, cudaStream_t stream) {
     return launch_rows<block_bwd<DT, VEC, V, FMT, FULL, CLUSTER>>(s, a.workers, smem, stream, a);
 }
 
-template <int DT, bool VEC, int V, int FMT>
-cudaError_t by_shape(const BlockBwd& a, bool full, cudaStream_t stream) {
+// SHARED: the width may take a cluster.
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool SHARED>
+cudaError_t by_shape(const BlockBwd& a, cudaStream_t stream) {
     const RowShape s = RowShape::of<V>(a.cols, V == 4 ? kBwdThreads : 2 * kBwdThreads, kBwdWarps);
-    if constexpr (V == 4 || DT == kF32) {
-        if (s.cluster > 1)
-            return full ? launch<DT, VEC, V, FMT, true, true>(a, s, stream)
-                        : launch<DT, VEC, V, FMT, false, true>(a, s, stream);
-    }
-    return full ? launch<DT, VEC, V, FMT, true, false>(a, s, stream) : launch<DT, VEC, V, FMT, false, false>(a, s, stream);
+    if constexpr (SHARED)
+        if (s.cluster > 1) return launch<DT, VEC, V, FMT, FULL, true>(a, s, stream);
+    return launch<DT, VEC, V, FMT, FULL, false>(a, s, stream);
 }
 
 // Segments a warp, by measurement (bf16 from e4m3): with all four sums of
@@ -756,13 +754,17 @@ cudaError_t by_shape(const BlockBwd& a, bool full, cudaStream_t stream) {
 // always (16384 x 1024: 59 and 52).
 // In fp32 four take too much shared memory for more than one small block an SM:
 // two (3001 x 4096 kept: 131 and 111 us), and clusters above 4096 columns.
-template <int DT, bool VEC, int FMT>
-cudaError_t by_width(const BlockBwd& a, bool full, cudaStream_t stream) {
-    if (a.cols <= 2048 && ((full && a.cols <= 1024) || a.rows < 16 * a.workers))
-        return by_shape<DT, VEC, 1, FMT>(a, full, stream);
-    if constexpr (DT != kF32)
-        if (a.cols > (full ? 1024 : 4096)) return by_shape<DT, VEC, 4, FMT>(a, full, stream);
-    return by_shape<DT, VEC, 2, FMT>(a, full, stream);
+template <int DT, bool VEC, int FMT, bool FULL>
+cudaError_t by_width(const BlockBwd& a, cudaStream_t stream) {
+    if (a.cols <= 2048 && ((FULL && a.cols <= 1024) || a.rows < 16 * a.workers))
+        return by_shape<DT, VEC, 1, FMT, FULL, false>(a, stream);
+    if constexpr (DT == kF32) {
+        return by_shape<DT, VEC, 2, FMT, FULL, true>(a, stream);
+    } else {
+        if constexpr (!FULL)
+            if (a.cols <= 4096) return by_shape<DT, VEC, 2, FMT, FULL, false>(a, stream);
+        return by_shape<DT, VEC, 4, FMT, FULL, true>(a, stream);
+    }
 }
 
 // vec: 16-byte accesses; ring: tensors on 16-byte boundaries.
@@ -771,8 +773,8 @@ cudaError_t by_alignment(const BlockBwd& a, bool vec, bool ring, cudaStream_t st
     count_launches(1);
     const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.dbeta_post || a.dbeta_pre ||
                       (a.dgate && a.beta_post);
-    if (vec) return by_width<DT, true, FMT>(a, full, stream);
-    if (ring) return by_width<DT, false, FMT>(a, full, stream);
+    if (vec) return full ? by_width<DT, true, FMT, true>(a, stream) : by_width<DT, true, FMT, false>(a, stream);
+    if (ring) return full ? by_width<DT, false, FMT, true>(a, stream) : by_width<DT, false, FMT, false>(a, stream);
     const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kBwdWarps);
     return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream) : launch_any<DT, FMT, false>(a, s, stream);
 }

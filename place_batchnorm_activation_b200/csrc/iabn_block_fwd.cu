@@ -368,40 +368,46 @@ cudaError_t launch(const BlockFwd& a, const RowShape& s, cudaStream_t stream, in
     return launch_rows<block_fwd<DT, VEC, V, FMT, FULL, CLUSTER>>(s, need < most ? need : most, smem, stream, a);
 }
 
-template <int DT, bool VEC, int V, int FMT>
-cudaError_t by_shape(const BlockFwd& a, bool full, cudaStream_t stream, int sms) {
+// SHARED: the width may take a cluster.
+template <int DT, bool VEC, int V, int FMT, bool FULL, bool SHARED>
+cudaError_t by_shape(const BlockFwd& a, cudaStream_t stream, int sms) {
     const RowShape s = RowShape::of<V>(a.cols, kFwdThreads, kFwdWarps);
-    if constexpr (V == 4 || DT == kF32 || !VEC) {
-        if (s.cluster > 1)
-            return full ? launch<DT, VEC, V, FMT, true, true>(a, s, stream, sms)
-                        : launch<DT, VEC, V, FMT, false, true>(a, s, stream, sms);
-    }
-    return full ? launch<DT, VEC, V, FMT, true, false>(a, s, stream, sms)
-                : launch<DT, VEC, V, FMT, false, false>(a, s, stream, sms);
+    if constexpr (SHARED)
+        if (s.cluster > 1) return launch<DT, VEC, V, FMT, FULL, true>(a, s, stream, sms);
+    return launch<DT, VEC, V, FMT, FULL, false>(a, s, stream, sms);
 }
 
-// vec: 16-byte accesses; ring: tensors on 16-byte boundaries.
+// vec: 16-byte accesses.
 // Segments a warp, by measurement: two up to 4096 columns (16384 x 4096 bf16,
 // e4m3: 119 us, with four 125), four above, which keep a row of up to 8192 in
 // one block (8192 x 8192: 129 us, 165 with two and a cluster of two blocks).
 // In fp32 four segments and the shifts exceed a block's shared memory: two.
+template <int DT, int FMT, bool FULL>
+cudaError_t by_width(const BlockFwd& a, bool vec, cudaStream_t stream, int sms) {
+    constexpr int kWide = DT == kF32 && FULL ? 2 : 4;
+    if (vec && a.cols <= 4096) return by_shape<DT, true, 2, FMT, FULL, false>(a, stream, sms);
+    if (vec) return by_shape<DT, true, kWide, FMT, FULL, true>(a, stream, sms);
+    return by_shape<DT, false, 2, FMT, FULL, true>(a, stream, sms);
+}
+
+// ring: tensors on 16-byte boundaries.
 template <int DT, int FMT>
-cudaError_t by_width(const BlockFwd& a, bool vec, bool ring, cudaStream_t stream, int sms) {
+cudaError_t by_norms(const BlockFwd& a, bool vec, bool ring, cudaStream_t stream, int sms) {
     count_launches(1);
+    if (!ring) {
+        const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kFwdWarps);
+        return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream, sms)
+                             : launch_any<DT, FMT, false>(a, s, stream, sms);
+    }
     const bool full = a.post == kNormLayer || a.pre == kNormLayer || a.beta_post || a.beta_pre;
-    if (vec && (a.cols <= 4096 || (DT == kF32 && full))) return by_shape<DT, true, 2, FMT>(a, full, stream, sms);
-    if (vec) return by_shape<DT, true, 4, FMT>(a, full, stream, sms);
-    if (ring) return by_shape<DT, false, 2, FMT>(a, full, stream, sms);
-    const RowShape s = RowShape::of<kAnyV>(a.cols, 256, kFwdWarps);
-    return s.cluster > 1 ? launch_any<DT, FMT, true>(a, s, stream, sms)
-                         : launch_any<DT, FMT, false>(a, s, stream, sms);
+    return full ? by_width<DT, FMT, true>(a, vec, stream, sms) : by_width<DT, FMT, false>(a, vec, stream, sms);
 }
 
 template <int DT>
 cudaError_t by_format(const BlockFwd& a, bool vec, bool ring, cudaStream_t s, int sms) {
-    if (!a.q_post && !a.q_pre) return by_width<DT, kNoCodes>(a, vec, ring, s, sms);
-    return a.format == kE4M3 ? by_width<DT, kE4M3>(a, vec, ring, s, sms)
-                             : by_width<DT, kInt8>(a, vec, ring, s, sms);
+    if (!a.q_post && !a.q_pre) return by_norms<DT, kNoCodes>(a, vec, ring, s, sms);
+    return a.format == kE4M3 ? by_norms<DT, kE4M3>(a, vec, ring, s, sms)
+                             : by_norms<DT, kInt8>(a, vec, ring, s, sms);
 }
 
 }  // namespace

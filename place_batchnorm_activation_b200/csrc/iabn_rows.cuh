@@ -352,7 +352,7 @@ __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {   // of raw_amax: as
     return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
 }
 
-// N = 1, 2 or 4 groups at once (VEC): m[i] is the lane's own largest magnitude
+// N = 2 or 4 groups at once (VEC): m[i] is the lane's own largest magnitude
 // in group i of its half-warp.  The sixteen lanes halve the number of groups
 // that each carries while they reduce, so that four reductions cost five
 // exchanges in place of sixteen, and the N divisions are one.  Returns every
@@ -361,7 +361,7 @@ __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {   // of raw_amax: as
 template <int FMT, int DT, int N>
 __device__ __forceinline__ float group_scales(const uint32_t (&m)[N], int lane, float (&by)[N]) {
     const bool hi = lane & 8, odd = lane & 4;
-    uint32_t a = m[0];
+    uint32_t a;
     if constexpr (N == 4) {
         a = hi ? m[2] : m[0];
         uint32_t b = hi ? m[3] : m[1];
@@ -370,10 +370,7 @@ __device__ __forceinline__ float group_scales(const uint32_t (&m)[N], int lane, 
         const uint32_t give = odd ? a : b;
         a = max(odd ? b : a, __shfl_xor_sync(0xffffffffu, give, 4));
     } else {
-        if constexpr (N == 2)
-            a = max(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], 8));
-        else
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        a = max(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], 8));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
     }
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
@@ -382,13 +379,13 @@ __device__ __forceinline__ float group_scales(const uint32_t (&m)[N], int lane, 
     group_scale<FMT>(amax_bits<DT>(a), scale, mine);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        by[i] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) | i * (16 / N));
+        by[i] = __shfl_sync(0xffffffffu, mine, (lane & 16) | i * (16 / N));
     return scale;
 }
 // Which of the N groups a lane carries, and whether it is the one to write it.
 template <int N>
 __device__ __forceinline__ int group_carried(int lane) {
-    return N == 4 ? (lane >> 2) & 3 : N == 2 ? (lane >> 3) & 1 : 0;
+    return N == 4 ? (lane >> 2) & 3 : (lane >> 3) & 1;
 }
 template <int N>
 __device__ __forceinline__ bool group_writer(int lane) {
