@@ -134,6 +134,8 @@ class _Call:
     __slots__ = ("T", "device", "rows", "cols", "numel", "dtype", "storage")
 
     def __init__(self, first, name: str):
+        if first is None:
+            _raise(f"{name} is needed")
         device = first.get_device()
         if device < 0:
             _raise(f"{name} is not on a CUDA device")
@@ -162,8 +164,9 @@ class _Call:
         if t.dtype != self.dtype or t.get_device() != self.device or t.numel() != self.numel \
                 or not t.is_contiguous():
             self._refuse(t, name, self.dtype, self.numel)
-        if t.shape[-1] != self.cols:
-            _raise(f"{name}: {tuple(t.shape)} has not {self.cols} columns")
+        shape = t.shape
+        if not shape or shape[-1] != self.cols:
+            _raise(f"{name}: {tuple(shape)} has not {self.cols} columns")
         return t.data_ptr()
 
     def floats(self, t, name: str, numel: int):
@@ -177,6 +180,8 @@ class _Call:
 
     def strided(self, t, name: str):
         """(pointer, row stride) of a tensor of the first one's type and size."""
+        if t is None:
+            _raise(f"{name} is needed")
         if t.dtype != self.dtype or t.get_device() != self.device:
             _raise(f"{name}: type {t.dtype} on {t.device}, not as the others")
         rows, cols, ld = _rows_of(t, name)
@@ -294,6 +299,8 @@ def new_block_norm_workspace(rows: int, cols: int, rows_per_gate: int = 0, devic
 
 
 def _workspace(c: _Call, ws):
+    if ws is None:
+        _raise("workspace is needed")
     if ws.get_device() != c.device or ws.dtype != c.T.uint8 or not ws.is_contiguous():
         _raise("workspace: not a contiguous uint8 tensor on the device of the others")
     return ws.data_ptr(), ws.numel()

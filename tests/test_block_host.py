@@ -319,6 +319,19 @@ def test_binding_refuses_cpu_tensors():
             call()
 
 
+def test_binding_refuses_a_missing_tensor():
+    x = torch.zeros(4, 64)
+    for call in (lambda: iabn.block_norm_forward(x, None, x, x), lambda: iabn.block_norm_forward_checkpoint8(x, None, x, x),
+                 lambda: iabn.block_norm_backward(x, x, x, x, None, x, x),
+                 lambda: iabn.block_norm_backward_checkpoint8(x, x, x, x, None, x, x),
+                 lambda: iabn.gated_forward(x, x, None), lambda: iabn.gated_backward(x, x, None, x, x),
+                 lambda: iabn.gated_forward_checkpoint8(x, x, None, x, x, x, x),
+                 lambda: iabn.gated_backward_checkpoint8(x, x, x, x, None, x, x),
+                 lambda: iabn.checkpoint8_store(None, x, x), lambda: iabn.checkpoint8_load(x, x, None)):
+        with pytest.raises(iabn.IabnError, match="is needed"):
+            call()
+
+
 def test_binding_rows_of():
     from place_batchnorm_activation_b200.block import _rows_of
     p = torch.zeros(6, 5, 20)

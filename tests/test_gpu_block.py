@@ -832,3 +832,16 @@ def test_constant_rows_of_large_values(cols, dtype, value):
     want = (w - w.mean()) * ((w - w.mean()).square().mean() + EPS["eps_post"]) ** -0.5
     step = torch.finfo(dtype).eps
     assert ((got["h_out"][2:].double() - want).abs() <= (step + 1e-5) * (1 + want.abs())).all()
+
+
+def test_binding_refuses_missing_tensors_and_scalars():
+    x = torch.zeros(4, 256, dtype=BF16, device="cuda")
+    y = [torch.empty_like(x) for _ in range(4)]
+    f, tiny, scalar = torch.zeros(4, device="cuda"), torch.zeros(1, 1, device="cuda"), torch.zeros((), device="cuda")
+    for call in (lambda: iabn.block_norm_backward(x, x, x, x, y[0], y[1], None, rstd_post=f, rstd_pre=f),
+                 lambda: iabn.gated_forward(x, None, y[0]), lambda: iabn.gated_forward(None, x, y[0]),
+                 lambda: iabn.gated_backward(x, x, x, None, y[0]), lambda: iabn.gated_backward(x, x, x, y[0], None),
+                 lambda: iabn.gated_backward(None, None, x, y[0], y[1]),
+                 lambda: iabn.block_norm_forward(scalar, tiny, torch.empty_like(tiny), torch.empty_like(tiny))):
+        with pytest.raises(iabn.IabnError):
+            call()
