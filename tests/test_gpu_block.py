@@ -845,3 +845,170 @@ def test_binding_refuses_missing_tensors_and_scalars():
                  lambda: iabn.block_norm_forward(scalar, tiny, torch.empty_like(tiny), torch.empty_like(tiny))):
         with pytest.raises(iabn.IabnError):
             call()
+
+
+@pytest.mark.parametrize("dtype,form", [(BF16, None), (F16, E4M3), (F32, None)])
+@pytest.mark.parametrize("cols,rows", [(1, 300), (7, 700), (73, 400), (1021, 333), (2049, 150), (4104, 60), (9001, 20),
+                                       (10240, 20), (20001, 7), (32768, 5)])
+def test_in_place_at_any_width(cols, rows, dtype, form):
+    """Outputs over inputs where a warp's copies take in words of its
+    neighbours' rows, and where a cluster shares a row."""
+    per = rows // 2
+    o = params(rows, cols, LAYER, LAYER, True, per, True, 1)
+    u, h = values(rows, cols, dtype, 2), values(rows, cols, dtype, 3, 2.0)
+    want = run_forward(u, h, o, form)
+    call = iabn.block_norm_forward if form is None else iabn.block_norm_forward_checkpoint8
+    kept = {k: torch.empty_like(v) for k, v in want.items() if k not in ("h_out", "n")}
+    for swap in (False, True):
+        u2, h2 = u.clone(), h.clone()
+        ho, n = (u2, h2) if swap else (h2, u2)
+        call(u2, h2, ho, n, **{**EPS, **o}, **kept)
+        assert torch.equal(ho, want["h_out"]) and torch.equal(n, want["n"]), swap
+        for k, v in kept.items():
+            assert torch.equal(v.view(torch.uint8), want[k].view(torch.uint8)), k
+    dh_out, dn = values(rows, cols, dtype, 4, 0.1), values(rows, cols, dtype, 5, 0.1)
+    o["beta_pre"] = None
+    ws = iabn.new_block_norm_workspace(rows, cols, per, device="cuda")
+    a = {k: o[k] for k in ("post", "pre", "rows_per_gate", "residual_scale", "gamma_post", "beta_post", "gate", "gamma_pre")}
+    if form is None:
+        stats = {k: want[k] for k in ("mean_post", "rstd_post", "mean_pre", "rstd_pre")}
+        src, pairs = (u, want["h_out"]), ((0, 1), (1, 0), (2, 3), (3, 2), (0, 2), (3, 1))
+        back = run_backward(*src, dh_out, dn, o, stats)
+    else:
+        stats = {k: want[k] for k in ("rstd_post", "rstd_pre")}
+        src, pairs = ((want["q_post"], want["scale_post"]), (want["q_pre"], want["scale_pre"])), ((0, 1), (1, 0))
+        back = run_backward(*src, dh_out, dn, o, stats)
+    grads = {k: torch.empty_like(v) for k, v in back.items() if k not in ("dh", "du")}
+    for i, j in pairs:
+        t = [dh_out.clone(), dn.clone()] + ([s.clone() for s in src] if form is None else [])
+        if form is None:
+            iabn.block_norm_backward(t[2], t[3], t[0], t[1], t[i], t[j], ws, **stats, **a, **grads)
+        else:
+            iabn.block_norm_backward_checkpoint8(src[0][0], src[1][0], t[0], t[1], t[i], t[j], ws, scale_post=src[0][1],
+                                                 scale_pre=src[1][1], **stats, **a, **grads)
+        for k, v in (grads | {"dh": t[i], "du": t[j]}).items():
+            assert torch.equal(v.view(torch.uint8), back[k].view(torch.uint8)), (k, i, j)
+    # the gated activation over its own inputs, packed and apart
+    p, dz = values(rows, 2 * cols, dtype, 6), values(rows, cols, dtype, 7)
+    want, z = torch.empty_like(p), torch.empty_like(dz)
+    iabn.gated_backward(p[:, :cols], p[:, cols:], dz, want[:, :cols], want[:, cols:], z=z)
+    for over in (0, 1):
+        a, b = p[:, :cols].contiguous(), p[:, cols:].contiguous()
+        iabn.gated_forward(a, b, (a, b)[over])
+        assert torch.equal((a, b)[over], z), over
+    iabn.gated_backward(p[:, :cols], p[:, cols:], dz, p[:, :cols], p[:, cols:], z=dz)
+    assert torch.equal(p, want) and torch.equal(dz, z)
+
+
+@pytest.mark.parametrize("form,dtype", [(None, F32), (INT8, BF16), (E4M3, F32)])
+@pytest.mark.parametrize("cols", [72, 73, 264, 1021, 2048, 2049, 8192, 9001, 12000])
+def test_a_bad_row_stays_in_its_row_backward(cols, form, dtype):
+    """NaN and infinities in a row's gradients, statistics or scales change no
+    bit of the other rows' gradients, nor of the gates that other rows have;
+    the sums over rows that a bad element enters are NaN or infinite there."""
+    rows, per = 24, 6
+    o = params(rows, cols, LAYER, LAYER, True, per, True, 1)
+    u, h = values(rows, cols, dtype, 2), values(rows, cols, dtype, 3)
+    f = run_forward(u, h, o, form)
+    o["beta_pre"] = torch.zeros(cols, device="cuda")
+    dh_out, dn = values(rows, cols, dtype, 4, 0.1), values(rows, cols, dtype, 5, 0.1)
+    names = ("mean_post", "rstd_post", "mean_pre", "rstd_pre") if form is None else ("rstd_post", "rstd_pre")
+    stats = {k: f[k] for k in names}
+    src = (u, f["h_out"]) if form is None else ((f["q_post"], f["scale_post"]), (f["q_pre"], f["scale_pre"]))
+    clean = run_backward(*src, dh_out, dn, o, stats)
+    bad_dn, bad_dh = dn.clone(), dh_out.clone()
+    bad_dn[1, cols // 2], bad_dn[4, cols - 1] = math.nan, math.inf
+    bad_dh[2, 0] = -math.inf
+    bad_stats = {k: v.clone() for k, v in stats.items()}
+    bad_stats["rstd_pre"][12] = math.nan
+    if form is None:
+        bad_src = (u.clone(), f["h_out"])
+        bad_src[0][13, cols // 3] = math.inf
+    else:
+        bad_src = ((f["q_post"], f["scale_post"].clone()), src[1])
+        bad_src[0][1][13, -1] = math.nan
+    got = run_backward(*bad_src, bad_dh, bad_dn, o, bad_stats)
+    bad = (1, 2, 4, 12, 13)
+    rest = [r for r in range(rows) if r not in bad]
+    for k in ("dh", "du"):
+        assert torch.equal(got[k][rest], clean[k][rest]), k
+        assert not torch.isfinite(got["du"][list(bad)].float()).all(-1).any(), k
+    assert torch.isnan(got["dh"][[1, 12]]).all()
+    # an infinite g makes both means infinite: g - inf - x (+-inf) is infinite or NaN in every column
+    assert not torch.isfinite(got["dh"][4]).any()
+    # gate rows 1 and 3 (rows 6-11 and 18-23) have no bad row
+    assert torch.equal(got["dgate"][[1, 3]], clean["dgate"][[1, 3]])
+    assert not torch.isfinite(got["dgate"][0]).any()
+    assert torch.isnan(got["dbeta_pre"][cols // 2]) and not torch.isfinite(got["dbeta_pre"][cols - 1])
+    if cols > 8:
+        c = [k for k in range(cols) if k not in (cols // 2, cols - 1)]
+        assert torch.equal(got["dbeta_pre"][c], clean["dbeta_pre"][c])
+
+
+def test_two_to_the_31_rows():
+    """The most rows that a call may have: the last rows, the gate rows that end
+    with them and their sums."""
+    rows, per = (1 << 31) - 1, 1 << 30
+    dh_out = torch.zeros(rows, 1, dtype=BF16, device="cuda")
+    u = torch.ones(rows, 1, dtype=BF16, device="cuda")
+    spots = [0, 1, 8, per - 1, per, per + 9, rows - 10, rows - 2, rows - 1]
+    for i, r in enumerate(spots):
+        dh_out[r], u[r] = i + 1.0, 2.0
+    gate, dgate = torch.tensor([[0.5], [4.0]], device="cuda"), torch.empty(2, 1, device="cuda")
+    ws = iabn.new_block_norm_workspace(rows, 1, per, device="cuda")
+    # both in place: dh over dh_out, du over u
+    iabn.block_norm_backward(u, None, dh_out, None, dh_out, u, ws, gate=gate, dgate=dgate, post=NONE, pre=NONE,
+                             rows_per_gate=per, residual_scale=2.0)
+    for i, r in enumerate(spots):
+        assert dh_out[r].item() == 2.0 * (i + 1) and u[r].item() == (0.5 if r < per else 4.0) * (i + 1), r
+    assert int(torch.count_nonzero(dh_out)) == len(spots) == int(torch.count_nonzero(u))
+    # t u over the gate's rows: 2 (1 + .. + 4) and 2 (5 + .. + 9)
+    assert dgate.view(-1).tolist() == [20.0, 70.0]
+    # and forward: n = h/|h| of single columns
+    h, n, r = u, dh_out, torch.empty(rows, device="cuda")
+    iabn.block_norm_forward(None, h, None, n, rstd_pre=r, post=NONE, pre=RMS, eps_pre=0.25)
+    for i, k in enumerate(spots):
+        v = (0.5 if k < per else 4.0) * (i + 1)
+        assert abs(n[k].item() - v / math.sqrt(v * v + 0.25)) < 2.0 ** -8 and abs(r[k].item() * math.sqrt(v * v + 0.25) - 1) < 1e-5
+    assert int(torch.count_nonzero(n)) == len(spots) and r[7].item() == 2.0
+
+
+def test_the_same_bits_at_a_training_size():
+    """16384 x 4096 with RMS norms and e4m3 codes: again and again the same bits,
+    whatever runs between; and the codes are the stated rounding of the values
+    that the kernel's own statistics give (those of another summation order may
+    fall on the other side of a tie)."""
+    rows, cols = 16384, 4096
+    r = lambda s: torch.randn(rows, cols, generator=torch.Generator("cuda").manual_seed(s), device="cuda")  # noqa: E731
+    u, h, other = r(1).to(BF16), (2 * r(2)).to(BF16), r(3).to(BF16)
+    gamma, gate = torch.rand(cols, device="cuda") + 0.5, torch.rand(1, cols, device="cuda")
+    new = lambda dtype: torch.empty(rows, cols, dtype=dtype, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+
+    def outputs():
+        return dict(h_out=new(BF16), n=new(BF16), q_post=new(E4M3), q_pre=new(E4M3), scale_post=f32(rows, 32),
+                    scale_pre=f32(rows, 32), rstd_post=f32(rows), rstd_pre=f32(rows))
+
+    def call(x, out, **kw):
+        k = {n: v for n, v in out.items() if n not in ("h_out", "n")}
+        iabn.block_norm_forward_checkpoint8(x, h, out["h_out"], out["n"], gamma_post=gamma, gate=gate, **k, **kw)
+
+    first, again, noise, side = outputs(), outputs(), outputs(), torch.cuda.Stream()
+    call(u, first)
+    torch.cuda.synchronize()
+    for turn in range(6):
+        for v in again.values():
+            v.view(torch.uint8).fill_(0xff)
+        call(other, noise, **({"stream": side} if turn % 2 else {}))
+        call(u, again)
+        torch.cuda.synchronize()
+        for k in first:
+            assert torch.equal(first[k].view(torch.uint8), again[k].view(torch.uint8)), (turn, k)
+    some = slice(None, None, 257)
+    uhat = u[some].float() * first["rstd_post"][some, None]
+    q, _ = ref.quantise(uhat.cpu(), E4M3)
+    assert torch.equal(q.float(), first["q_post"][some].cpu().float())
+    # (a residual scale of 1: the sum is rounded once whether or not it is fused)
+    hout = h[some].float() + uhat * (gamma * gate[0])
+    q, _ = ref.quantise((hout * first["rstd_pre"][some, None]).cpu(), E4M3)
+    assert torch.equal(q.float(), first["q_pre"][some].cpu().float())
