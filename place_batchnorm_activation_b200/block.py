@@ -214,7 +214,7 @@ class _Call:
     def gate(self, t, name: str, rows_per_gate: int):
         if t is None:
             return None
-        if rows_per_gate < 0:
+        if not 0 <= rows_per_gate < 1 << 63:   # (more would be cut to 64 bits)
             _raise(f"rows_per_gate = {rows_per_gate}")
         rows = 1 if rows_per_gate == 0 else -(-self.rows // rows_per_gate)
         return self.floats(t, name, rows * self.cols)

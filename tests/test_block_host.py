@@ -332,6 +332,16 @@ def test_binding_refuses_a_missing_tensor():
             call()
 
 
+def test_binding_refuses_more_rows_a_gate_than_64_bits_hold():
+    """A descriptor would cut 2^64 + 3 to 3, and more gate rows would be read than there are."""
+    from place_batchnorm_activation_b200.block import _Call
+    c = object.__new__(_Call)
+    c.rows, c.cols = 16, 64
+    for per in (-1, 1 << 63, (1 << 64) + 3):
+        with pytest.raises(iabn.IabnError, match="rows_per_gate"):
+            c.gate(torch.zeros(1, 64), "gate", per)
+
+
 def test_binding_rows_of():
     from place_batchnorm_activation_b200.block import _rows_of
     p = torch.zeros(6, 5, 20)
