@@ -1012,3 +1012,84 @@ def test_the_same_bits_at_a_training_size():
     hout = h[some].float() + uhat * (gamma * gate[0])
     q, _ = ref.quantise((hout * first["rstd_pre"][some, None]).cpu(), E4M3)
     assert torch.equal(q.float(), first["q_pre"][some].cpu().float())
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch, place_batchnorm_activation_b200 as iabn
+rows, cols = {rows}, {cols}
+new = lambda *s: torch.randn(*s, device="cuda")
+u, h, dh_out, dn = (new(rows, cols).bfloat16() for _ in range(4))
+beta, gate = new(cols), new(2, cols)
+out = {{k: torch.empty_like(u) for k in ("h_out", "n", "dh", "du", "z", "da", "db")}}
+stats = {{k: torch.empty(rows, device="cuda") for k in ("mean_post", "rstd_post", "mean_pre", "rstd_pre")}}
+grads = {{"dgamma_post": torch.empty(cols, device="cuda"), "dgate": torch.empty(2, cols, device="cuda")}}
+per, ws = -(-rows // 2), iabn.new_block_norm_workspace(rows, cols, -(-rows // 2), device="cuda")
+q, s = torch.empty_like(u, dtype=torch.int8), torch.empty(rows, -(-cols // 128), device="cuda")
+def call():
+    how = dict(post=2, pre=2, rows_per_gate=per, beta_post=beta, gate=gate)
+    iabn.block_norm_forward(u, h, out["h_out"], out["n"], **stats, **how)
+    iabn.block_norm_backward(u, out["h_out"], dh_out, dn, out["dh"], out["du"], ws, **stats, **grads, **how)
+    iabn.gated_backward(u, h, dn, out["da"], out["db"], z=out["z"])
+    iabn.checkpoint8_store(out["n"], q, s)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in [*out.values(), *stats.values(), *grads.values(), q, s]]
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+           for a, b in zip(got, [*out.values(), *stats.values(), *grads.values(), q, s]))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 4096), (40, 1021), (9, 9000)])
+def test_a_first_call_inside_a_capture(rows, cols):
+    """A program's first calls of the operators may be the ones it captures."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE.format(rows=rows, cols=cols)], cwd=root, timeout=120,
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_more_gate_rows_than_the_column_pass_has_blocks():
+    """A gate row a token, 9001 of them, and the sums over them."""
+    one(9001, 40, BF16, RMS, LAYER, True, 1, True, E4M3, seed=3)
+    one(9001, 9, F32, LAYER, RMS, True, 2, True, None, seed=4)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [40, 1024, 4096, 9000])
+def test_outputs_off_16_byte_boundaries(cols, dtype):
+    """Inputs on 16-byte boundaries, one output or many of them not."""
+    rows = 11
+    o = params(rows, cols, RMS, LAYER, True, 4, True, 1)
+    u, h = values(rows, cols, dtype, 2), values(rows, cols, dtype, 3, 2.0)
+    dh_out, dn = values(rows, cols, dtype, 4, 0.1), values(rows, cols, dtype, 5, 0.1)
+
+    class Off(Buffers):
+        def __init__(self, which):
+            super().__init__()
+            self.which = which
+
+        def new(self, name, shape, dt, fill=None):
+            if name not in self.which:
+                return super().new(name, shape, dt, fill)
+            n = math.prod(shape)
+            flat = super().new(name, (n + 1,), dt)
+            return flat[1:].view(shape)
+
+    for form in (None, INT8):
+        for which in (("n",), ("h_out", "n", "q_post", "q_pre", "dh", "du", "dgamma_post", "dgate")):
+            got = run_forward(u, h, o, form, Off(which))
+            check_forward(u, h, o, form, got, f"off {which}")
+            stats = {k: got[k] for k in ("mean_pre", "rstd_post", "rstd_pre") if got.get(k) is not None}
+            src = (u, got["h_out"]) if form is None else ((got["q_post"], got["scale_post"]), (got["q_pre"], got["scale_pre"]))
+            back = run_backward(*src, dh_out, dn, o | {"beta_pre": None}, stats, Off(which))
+            check_backward(back, backward_want(*src, dh_out, dn, o, stats), dtype, f"off {which}")
