@@ -52,8 +52,10 @@ extern "C" {
  * group of a row may be shorter): codes [rows, cols], scales
  * [rows, ceil(cols / IABN_Q8_GROUP)], both contiguous.  With amax the group's
  * largest magnitude and Q the format's (448 or 127),
- *   scale = amax / Q,  code = round_to_nearest_even(x * (Q / amax)),
- *   value = code * scale.
+ *   scale = amax * (1 / Q),  code = round_to_nearest_even(x * (Q / amax)),
+ *   value = code * scale,
+ * 1 / Q, Q / amax and the three products each rounded to float32 (so scale may
+ * be the float next to amax / Q).
  * A group whose amax is below 2^-110 is kept as zeros with scale 0.  A group
  * that holds a NaN or an infinity gets the scale NaN, so that all its values
  * read back as NaN.
@@ -61,6 +63,7 @@ extern "C" {
  *                 2^-4 of itself (or scale * 2^-10 where that is more).
  *   IABN_Q8_INT8  a value's error is at most scale / 2: the finer one where a
  *                 group's values are of one size.
+ * (Either error by itself; the five roundings to float32 add up to 2^-13 of it.)
  * ------------------------------------------------------------------------ */
 typedef enum { IABN_Q8_E4M3 = 0, IABN_Q8_INT8 = 1 } iabn_q8;
 #define IABN_Q8_GROUP 128

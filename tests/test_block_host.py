@@ -432,3 +432,29 @@ def test_reference_quantiser(form):
     bound = ref.code_bound(x.double(), torch.zeros_like(v), scale, form)
     assert ((v - x.double()).abs()[ok] <= bound[ok]).all()
     assert not torch.isnan(v[4, 128:]).any() and not torch.isnan(v[5, :256]).any()
+
+
+@pytest.mark.parametrize("form", [torch.float8_e4m3fn, torch.int8])
+def test_stated_errors_of_the_checkpoints(form):
+    """What the header says of a value's error, with the roundings to fp32: five
+    of 2^-24 each of a value that is at most 127 scales (int8), a half-step being
+    scale/2, or of 17/16 of a value whose half-step is 2^-4 of it, or of 2^-6
+    scales whose half-step is 2^-10 (e4m3): at most 5 * 254 * 2^-24 < 2^-13 of the
+    half-step.  The scale is amax * fl(1/Q): the float of amax / Q or the next one."""
+    top = ref.QMAX[form]
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(64, 512, generator=g) * torch.exp(2 * torch.randn(64, 512, generator=g))
+    amax = x.view(64, 4, 128).abs().amax(-1)
+    # values on the ties between two codes, where the error is a half-step
+    ties = torch.arange(0, 127, dtype=torch.float32) + 0.5
+    x[:32, :127] = ties * (amax[:32, :1] / 127.0)
+    amax = x.view(64, 4, 128).abs().amax(-1)
+    codes, scale = ref.quantise(x, form)
+    inverse = torch.tensor(1.0 / top)
+    assert torch.equal(scale, amax * inverse)
+    ulp = (scale.view(torch.int32) - (amax / top).view(torch.int32)).abs()
+    assert int(ulp.max()) == 1        # they do differ, and by no more
+    value = (codes.float() * scale.repeat_interleave(128, 1)).double()
+    wide = scale.double().repeat_interleave(128, 1)
+    half = wide / 2 if form == torch.int8 else torch.maximum(x.double().abs() * 2.0 ** -4, wide * 2.0 ** -10)
+    assert ((value - x.double()).abs() <= half * (1 + 2.0 ** -13)).all()
