@@ -19,9 +19,11 @@
 // registers of half the warps that an SM could hold, so what bounds it is the
 // latency between a row's reductions, then the instructions.
 // Measured (GPU time, B200): 16384 x 4096 bf16 RMS norms from e4m3 129 us (5.2
-// TB/s, floor 105); layer norms with shifts 163 us; 2048 x 8192 layer norms 66
-// us (floor 26); 3001 x 1021 kept fp32 32 us (floor 11.5).  The column pass is 4
-// to 6 us of these.
+// TB/s, floor 105), kept 139 us (floor 125); layer norms with or without shifts
+// 161 us; 16384 x 5120 RMS 209 us (floor 131: five warps an SM); 8192 x 4096 fp32
+// kept 218 us (floor 125); 2048 x 8192 layer norms 76 us (floor 26); 3001 x 1021
+// kept fp32 33 us (floor 11.5).  The row pass by itself is 122 us of the first,
+// 61 and 24 us of the last two; the rest is the column pass and its launch.
 #include "iabn_rows.cuh"
 
 namespace iabn {
@@ -787,8 +789,13 @@ cudaError_t by_format(const BlockBwd& a, bool vec, bool ring, bool codes, cudaSt
 
 }  // namespace
 
-// One wave of the row pass's blocks on 148 SMs: two a SM up to 4096 columns,
-// one above, where clusters of them share rows of more than 8192.
+// For the 16-bit types one wave of the row pass's blocks on 148 SMs: two an SM
+// up to 4096 columns, one above, where clusters of them share rows of more than
+// 8192.  fp32 takes the same number of workers, since the workspace's size does
+// not know the type; with its two segments a warp above 2048 columns a block of
+// six warps or more has an SM to itself and rows of more than 4096 columns take
+// clusters, so its 296 blocks are two waves (3001 x 4096 kept layer norms 101 us,
+// floor 46).
 int64_t block_bwd_workers(int64_t rows, int64_t cols) {
     const int64_t most = cols <= 4096 ? 296 : 148 / RowShape::of<4>((int)cols, kBwdThreads, kBwdWarps).cluster;
     return rows < 1 ? 1 : rows < most ? rows : most;

@@ -12,10 +12,11 @@
 // checkpoint groups.
 // Floor: 4 s bytes an element (s the storage size), 2 more with checkpoints.
 // Measured (GPU time, B200): 16384 x 4096 bf16, RMS norms, e4m3 checkpoints
-// 121 us (5.6 TB/s, floor 105 at the 6.43 TB/s of a copy); layer norms with
-// shifts 162 us; 8192 x 8192 128 us; 3001 x 1021 fp16 layer norms 14.1 us
-// (floor 3.8); 8 x 4096 without checkpoints 3.6 us, the launch's own time and
-// two reductions.
+// 121 us (5.6 TB/s, floor 105 at the 6.43 TB/s of a copy), nothing kept 93 us
+// (floor 83.5); layer norms 149 us, with shifts 163 us; 8192 x 8192 130 us;
+// 16384 x 5120 199 us (floor 131: five warps an SM); 8192 x 4096 fp32, nothing
+// kept, 129 us (floor 83.5); 3001 x 1021 fp16 layer norms 16 us (floor 3.8); 8 x
+// 4096 without checkpoints 3.6 us, the launch's own time and two reductions.
 #include "iabn_rows.cuh"
 
 namespace iabn {
@@ -379,9 +380,10 @@ cudaError_t by_shape(const BlockFwd& a, cudaStream_t stream, int sms) {
 
 // vec: 16-byte accesses.
 // Segments a warp, by measurement: two up to 4096 columns (16384 x 4096 bf16,
-// e4m3: 119 us, with four 125), four above, which keep a row of up to 8192 in
-// one block (8192 x 8192: 129 us, 165 with two and a cluster of two blocks).
-// In fp32 four segments and the shifts exceed a block's shared memory: two.
+// e4m3, compared on one box: 119 us, with four 125), four above, which keep a
+// row of up to 8192 in one block (8192 x 8192: 129 us, 165 with two and a cluster
+// of two blocks).  In fp32 four segments and the shifts exceed a block's shared
+// memory: two.  So have odd widths, which therefore take clusters above 4096.
 template <int DT, int FMT, bool FULL>
 cudaError_t by_width(const BlockFwd& a, bool vec, cudaStream_t stream, int sms) {
     constexpr int kWide = DT == kF32 && FULL ? 2 : 4;

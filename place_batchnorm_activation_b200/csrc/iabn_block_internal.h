@@ -46,14 +46,15 @@ struct BlockBwd {
     float* work;   // partial sums
     int64_t rows, rows_per_gate;
     int64_t gates;   // gate rows (1 without a gate)
-    int64_t workers; // CTAs of the row pass
+    int64_t workers; // blocks (clusters) of the row pass
     int cols, groups;
     int post, pre, format;
     float alpha;
 };
 
-// CTAs of the backward's row pass, and the partial-sum rows of `cols` floats
-// they need: two a worker (dn*xhat, dn) and two a (worker, gate row) pair
+// Workers of the backward's row pass (a block or a cluster of them; laid out for
+// 148 SMs), and the partial-sum rows of `cols` floats they need: two a worker
+// (dn*xhat, dn) and two a (worker, gate row) pair
 // (t*uhat, t), the pair (w, g) in slot w + g: workers take consecutive rows,
 // so from pair to pair at least one of the two grows.
 int64_t block_bwd_workers(int64_t rows, int64_t cols);

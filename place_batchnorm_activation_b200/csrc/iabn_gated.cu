@@ -9,10 +9,11 @@
 // Floor: 3 s bytes an element forward (2 more with checkpoints), 3 s + 2
 // backward from codes, s more for z.
 // Measured (GPU time, B200): 8192 x 14336 bf16 SiLU with int8 checkpoints,
-// forward 162 us (5.8 TB/s, floor 147), backward with z 194 us (floor 184);
-// storing 16384 x 5120 bf16 as e4m3 45 us (floor 39.5), loading 16384 x 4096
-// with a scale 36 us (floor 31.6); 777 x 2731 fp16 GELU backward 12 us (floor
-// 2.7: elements one by one, and erfc).
+// forward 163 us (5.8 TB/s, floor 147), backward with z 204 us (floor 184); GELU
+// by erfc 280 and 321 us; storing 16384 x 5120 bf16 as e4m3 44 us (floor 39.5),
+// loading 16384 x 4096 with a scale 36 us (floor 31.6); 777 x 2731 fp16 GELU
+// backward from e4m3 11 us (floor 2.7), SiLU 6.2 us, and in 2736 columns, eight
+// at a time, 7.9 and 4.6 us: erfc and elements one by one.
 #include "iabn_rows.cuh"
 
 namespace iabn {
@@ -21,8 +22,9 @@ void count_launches(int n);
 
 namespace {
 
-// e^x and 1/x for the 16-bit types: one special-function instruction each
+// 2^x and 1/x for the 16-bit types: one special-function instruction each
 // (relative error about 2^-22 and 2^-23), results below 2^-126 flushed to 0.
+// e^x is 2^(x log2 e), whose rounded argument adds about |x| 2^-24 to that.
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -107,9 +109,10 @@ struct Down {
 // Rows of a strip that are loaded before any is worked on, and blocks an SM:
 // with fewer bytes in flight HBM waits, with more the registers run out (8192 x
 // 14336 bf16, int8 checkpoints, forward: 2 rows and 4 blocks 182 us; 1 and 4
-// 193, 1 and 6 195, 2 and 3 189, 4 and 2 194, 4 and 3 186).  Elements one by
-// one take eight times the load instructions, so one row is ahead enough
-// (777 x 2731: 10.4 us, 13.1 with two).
+// 193, 1 and 6 195, 2 and 3 189, 4 and 2 194, 4 and 3 186; all before later
+// steps made each faster).  Elements one by one take eight times the load
+// instructions, so one row ahead is enough (777 x 2731, compared on one box: 10.4
+// us, 13.1 with two).
 constexpr int kVecAhead = 2;
 constexpr int kBlocks = 4;
 

@@ -707,7 +707,9 @@ struct RowShape {
 constexpr size_t kFreeShared = 46 * 1024;    // a block's dynamic shared memory without asking
 constexpr size_t kSharedAnSm = 227 * 1024;   // an SM's shared memory for blocks
 
-// Blocks an SM that a kernel with __launch_bounds__(256, `least`) may count on.
+// Blocks an SM that a kernel with __launch_bounds__(256, `least`) may count on
+// (whole blocks of what its registers are bounded for: one of five to seven
+// warps counts as one of eight).
 inline int blocks_an_sm(int least, int threads, size_t smem) {
     const int by_registers = least * 256 / threads;
     const int by_shared = (int)(kSharedAnSm / (smem + kRedFloats * sizeof(float) + 1024));
