@@ -1093,3 +1093,52 @@ def test_outputs_off_16_byte_boundaries(cols, dtype):
             src = (u, got["h_out"]) if form is None else ((got["q_post"], got["scale_post"]), (got["q_pre"], got["scale_pre"]))
             back = run_backward(*src, dh_out, dn, o | {"beta_pre": None}, stats, Off(which))
             check_backward(back, backward_want(*src, dh_out, dn, o, stats), dtype, f"off {which}")
+
+
+@pytest.mark.parametrize("dtype,form", [(BF16, None), (BF16, INT8), (F32, E4M3)])
+@pytest.mark.parametrize("cols", [264, 1021, 4096, 9000])
+def test_outputs_that_are_not_wanted(cols, dtype, form):
+    """Each optional output left out by itself: the others are the same bits.
+    (Layer norms, whose kernels do not depend on which sums are asked for.)"""
+    rows, per = 10, 4
+    o = params(rows, cols, LAYER, LAYER, True, per, True, 1)
+    u, h = values(rows, cols, dtype, 2), values(rows, cols, dtype, 3, 2.0)
+    full = run_forward(u, h, o, form)
+    names = [k for k in full if k not in ("h_out", "n")]
+    pairs = [(k,) for k in names if "_p" in k and k[:2] not in ("q_", "sc")]
+    pairs += [("q_post", "scale_post"), ("q_pre", "scale_pre")] if form is not None else []
+    call = iabn.block_norm_forward if form is None else iabn.block_norm_forward_checkpoint8
+    for left in [("h_out",), *pairs, tuple(n for n in names if form is None or n.startswith("rstd"))]:
+        out = {k: None if k in left else torch.empty_like(v) for k, v in full.items()}
+        call(u, h, out["h_out"], out["n"], **{**EPS, **o}, **{k: v for k, v in out.items() if k not in ("h_out", "n")})
+        for k, v in out.items():
+            assert v is None or torch.equal(v.view(torch.uint8), full[k].view(torch.uint8)), (left, k)
+    dh_out, dn = values(rows, cols, dtype, 4, 0.1), values(rows, cols, dtype, 5, 0.1)
+    o["beta_pre"] = torch.zeros(cols, device="cuda")
+    stats = {k: full[k] for k in (("mean_post", "rstd_post", "mean_pre", "rstd_pre") if form is None else ("rstd_post", "rstd_pre"))}
+    src = (u, full["h_out"]) if form is None else ((full["q_post"], full["scale_post"]), (full["q_pre"], full["scale_pre"]))
+    grads = ("dgamma_post", "dbeta_post", "dgate", "dgamma_pre", "dbeta_pre")
+    whole = run_backward(*src, dh_out, dn, o, stats)
+    check_backward(whole, backward_want(*src, dh_out, dn, o, stats), dtype, "whole")
+    for left in (*((g,) for g in grads), grads[:3], grads[3:], grads):
+        back = run_backward(*src, dh_out, dn, o, stats, want=[g for g in grads if g not in left])
+        assert set(whole) - set(back) == set(left)
+        for k, v in back.items():
+            assert torch.equal(v.view(torch.uint8), whole[k].view(torch.uint8)), (left, k)
+    # du not wanted
+    ws = iabn.new_block_norm_workspace(rows, cols, per, device="cuda")
+    a = {k: o[k] for k in ("post", "pre", "rows_per_gate", "residual_scale", "gamma_post", "beta_post", "gate", "gamma_pre")}
+    out = {k: torch.empty_like(v) for k, v in whole.items() if k != "du"}
+    g = {k: v for k, v in out.items() if k != "dh"}
+    if form is None:
+        iabn.block_norm_backward(*src, dh_out, dn, out["dh"], None, ws, **stats, **a, **g)
+    else:
+        iabn.block_norm_backward_checkpoint8(src[0][0], src[1][0], dh_out, dn, out["dh"], None, ws, scale_post=src[0][1],
+                                             scale_pre=src[1][1], **stats, **a, **g)
+    for k, v in out.items():
+        assert torch.equal(v.view(torch.uint8), whole[k].view(torch.uint8)), k
+    # no gradient through the residual stream: as one of zeros
+    zero = run_backward(*src, torch.zeros_like(dh_out), dn, o, stats)
+    none = run_backward(*src, None, dn, o, stats)
+    for k, v in none.items():
+        assert torch.equal(v, zero[k]), k
